@@ -1,4 +1,4 @@
-"""ctypes binding of libgdn (include/gdn.h, include/qsa.h): argument marshalling only.
+"""ctypes binding of libgdn (include/gdn.h, qsa.h, attn.h): argument marshalling only.
 
 Every step of the gated delta rule runs in libgdn's CUDA kernels; this module
 passes torch device pointers, sizes and the current CUDA stream through the C ABI
@@ -8,6 +8,7 @@ missing, or a tensor is not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -26,15 +27,28 @@ GDN_FLAG_GATE_LOGITS = 4
 GDN_QSA_R, GDN_QSA_DIM, GDN_QSA_ROPE_DIMS, GDN_QSA_HEADS = 4, 128, 64, 4
 GDN_QSA_MAX_BUDGET, GDN_QSA_MAX_SEQS, GDN_QSA_MAX_QUERIES = 4096, 4096, 4
 
-# every symbol include/gdn.h and include/qsa.h declare
+# paged cache and its attention (include/attn.h)
+GDN_ATTN_MAX_QUERIES, GDN_ATTN_MAX_LIST, GDN_ROPE_MAX_AXES = 8, 16384, 3
+GDN_ROPE_INTERLEAVED = 1
+
+# every symbol include/gdn.h, qsa.h and attn.h declare
 EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_decode_step",
             "gdn_get_device_error", "gdn_status_string", "gdn_prefill_static_scratch",
             "gdn_decode_multi", "gdn_backward", "gdn_backward_workspace_size",
             "gdn_qsa_compress", "gdn_qsa_index_workspace_size", "gdn_qsa_index_decode",
             "gdn_qsa_index_multi_workspace_size", "gdn_qsa_index_multi",
-            "gdn_set_wait_budget", "gdn_set_prefill_segment_tokens", "gdn_prefill_schedule")
+            "gdn_set_wait_budget", "gdn_set_prefill_segment_tokens", "gdn_prefill_schedule",
+            "gdn_kv_append", "gdn_attn_decode_workspace_size", "gdn_attn_decode",
+            "gdn_qsa_attn_decode")
 
 _lib = None
+
+
+class _PagedKVStruct(ctypes.Structure):          # gdn_paged_kv
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int)]
 
 
 class GdnError(RuntimeError):
@@ -89,6 +103,17 @@ def lib():
         L.gdn_set_wait_budget.restype = U32
         L.gdn_set_prefill_segment_tokens.argtypes = [I32]
         L.gdn_set_prefill_segment_tokens.restype = ctypes.c_int
+        KV = ctypes.POINTER(_PagedKVStruct)
+        L.gdn_kv_append.argtypes = [KV, P, P, P, P, I64, I64, I64, P, P, I32, I64, I32, P, I32, P,
+                                    P, I32, U32, P]
+        L.gdn_kv_append.restype = ctypes.c_int
+        L.gdn_attn_decode_workspace_size.argtypes = [I32, I32, I32, I32, ctypes.c_int]
+        L.gdn_attn_decode_workspace_size.restype = SZ
+        L.gdn_attn_decode.argtypes = [P, P, KV, P, P, I32, I32, I32, F, F, I32, P, SZ, P]
+        L.gdn_attn_decode.restype = ctypes.c_int
+        L.gdn_qsa_attn_decode.argtypes = [P, P, KV, P, I32, I32, P, P, I32, I32, I32, F, F, P, SZ,
+                                          P]
+        L.gdn_qsa_attn_decode.restype = ctypes.c_int
         L.gdn_get_device_error.argtypes = [P, P]
         L.gdn_get_device_error.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
@@ -468,3 +493,244 @@ def gdn_qsa_index_multi(q, q_pos, k_hat, cu_blocks, budget_blocks: int = 512, *,
         _dev(workspace, "workspace"), workspace.numel(), _stream(stream))
     _check(st, "gdn_qsa_index_multi")
     return block_idx, block_score, token_idx
+
+
+# ---------------------------------------------------- paged cache and its attention
+class PagedKV:
+    """A paged key-value cache: k, v [num_pages, page_size, H_kv, d] (float32 or bfloat16) and
+    page_table int32 [num_seqs, max_pages].  The object keeps the three tensors and the struct
+    the library reads; their contents may change at any time, the tensors themselves may not
+    (make another PagedKV for another table)."""
+
+    __slots__ = ("k", "v", "page_table", "dtype", "device", "H_kv", "d", "seqs", "code", "ref",
+                 "_struct")
+
+    def __init__(self, k, v, page_table):
+        code = _dtype_code(k)
+        if k.dim() != 4:
+            raise ValueError(f"k must be [num_pages, page_size, H_kv, d], got {tuple(k.shape)}")
+        if v.dtype != k.dtype:
+            raise TypeError(f"v must have k's dtype {k.dtype}, got {v.dtype}")
+        if v.shape != k.shape:
+            raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+        if page_table.dtype != torch.int32:
+            raise TypeError("page_table must be int32")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [num_seqs, max_pages]")
+        for name, t in (("k", k), ("v", v), ("page_table", page_table)):
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, k on {k.device}")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.dtype, self.device, self.code = k.dtype, k.device, code
+        num_pages, page_size, self.H_kv, self.d = k.shape
+        self.seqs = page_table.shape[0]
+        self._struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), num_pages,
+                                      page_table.shape[1], page_size, self.H_kv, self.d, code)
+        self.ref = ctypes.byref(self._struct)
+
+
+def _launch_stream(kv) -> int:
+    """The current stream; every operand was found on the cache's device before."""
+    if kv.device.type != "cuda":
+        raise ValueError("the cache must be in CUDA tensors (libgdn has no CPU path)")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _placed(fn):
+    """Run `fn` on the device of its first tensor and, when `stream` is given, with that stream
+    current, so that what the call allocates belongs to the stream it is used on."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if first.is_cuda:
+            if stream is not None:
+                if stream.device != first.device:
+                    raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
+                with torch.cuda.stream(stream):
+                    return fn(first, *args, **kw)
+            if first.device.index != torch.cuda.current_device():
+                with torch.cuda.device(first.device):
+                    return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _addr(t, name, dtype, shape, dev):
+    """Device address of an operand (None stays None) after checking type, shape, layout and
+    device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    return t.data_ptr()
+
+
+def _token_rows(t, name, dtype, T_total, heads, d, dev):
+    """Address and token stride of [T_total, heads, d] (or [B, T, heads, d]) whose heads and dims
+    are contiguous; tokens may lie further apart."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have the cache's dtype {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if t.dim() == 4 and t.stride(0) != t.shape[1] * t.stride(1) and t.shape[0] > 1:
+        raise ValueError(f"{name}'s tokens must be evenly spaced")
+    if t.dim() not in (3, 4) or t.shape[-1] != d or (heads is not None and t.shape[-2] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [.., {heads}, {d}]")
+    if t.numel() != T_total * t.shape[-2] * d:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {T_total} tokens")
+    if (t.stride(-1) != 1 or t.stride(-2) != d) and t.numel() > 0:
+        raise ValueError(f"{name}'s heads and dims must be contiguous")
+    return t.data_ptr(), t.stride(-3)
+
+
+def _sequences(x, cu_seqlens, kv):
+    """(T_total, num_seqs) of packed [T_total, H, d] with offsets, or dense [B, T, H, d]."""
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
+        if x.dim() != 3:
+            raise ValueError("packed tokens must be [T_total, heads, d]")
+        T_total, N = x.shape[0], cu_seqlens.numel() - 1
+    elif x.dim() == 4:
+        N = x.shape[0]
+        T_total = N * x.shape[1]
+    elif x.dim() == 3:
+        N, T_total = 1, x.shape[0]
+    else:
+        raise ValueError("tokens must be [T_total, heads, d] or [B, T, heads, d]")
+    if N > kv.seqs:
+        raise ValueError(f"page_table has {kv.seqs} rows for {N} sequences")
+    return T_total, N
+
+
+def rope_inv_freq(rope_dims: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The usual rotation frequencies base^(-2i / rope_dims) as gdn_kv_append takes them."""
+    i = torch.arange(0, rope_dims, 2, dtype=torch.float64)
+    return (float(base) ** (-i / rope_dims)).float().to(device)
+
+
+@_placed
+def gdn_kv_append(k, v, kv: PagedKV, cu_seqlens=None, pos0=None, *, q=None, q_out=None,
+                  inv_freq=None, rope_pos=None, rope_sections=None, interleaved: bool = False):
+    """Put a call's keys and values into the cache, the keys rotated on the way, and rotate its
+    queries.  k, v [T_total, H_kv, d] with cu_seqlens int32 [N + 1], or [B, T, H_kv, d]; tokens
+    may lie further apart than their heads (a slice of a fused projection).  pos0 int32 [N]:
+    position of each sequence's first token (None: 0).  inv_freq float32 [rope_dims / 2]
+    (None: no rotation); rope_pos int32 [n_axes, T_total] with rope_sections (a tuple of n_axes
+    frequency counts) rotates at other positions than the cache's.  Returns q_out (q's shape,
+    contiguous; it may be q itself), or None without q."""
+    dev, dt, d = kv.device, kv.dtype, kv.d
+    T_total, N = _sequences(k, cu_seqlens, kv)
+    kp, ks = _token_rows(k, "k", dt, T_total, kv.H_kv, d, dev)
+    vp, vs = _token_rows(v, "v", dt, T_total, kv.H_kv, d, dev)
+    qp, qs, qo, H_q = None, 0, None, 0
+    if q is not None:
+        qp, qs = _token_rows(q, "q", dt, T_total, None, d, dev)
+        H_q = q.shape[-2]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        qo = _addr(q_out, "q_out", dt, q.shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rope_dims, n_axes, sections = 0, 1, None
+    if inv_freq is not None:
+        rope_dims = 2 * inv_freq.numel()
+        if rope_sections is not None:
+            n_axes = len(rope_sections)
+            if n_axes < 1 or n_axes > GDN_ROPE_MAX_AXES:
+                raise ValueError(f"rope_sections must have 1 to {GDN_ROPE_MAX_AXES} entries")
+            if n_axes > 1 and rope_pos is None:
+                raise ValueError("several axes need rope_pos")
+            sections = (ctypes.c_int32 * n_axes)(*rope_sections)
+    elif rope_pos is not None or rope_sections is not None:
+        raise ValueError("rope_pos and rope_sections need inv_freq")
+    st = lib().gdn_kv_append(
+        kv.ref, kp, vp, qp, qo, ks, vs, qs,
+        _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev),
+        _addr(pos0, "pos0", torch.int32, (N,), dev), N, T_total, H_q,
+        _addr(inv_freq, "inv_freq", torch.float32, (rope_dims // 2,), dev), rope_dims,
+        _addr(rope_pos, "rope_pos", torch.int32, (n_axes, T_total), dev), sections, n_axes,
+        GDN_ROPE_INTERLEAVED if interleaved else 0, _launch_stream(kv))
+    _check(st, "gdn_kv_append")
+    return q_out
+
+
+def gdn_attn_decode_workspace_size(n_queries: int, H_q: int, H_kv: int, d: int,
+                                   dtype=torch.bfloat16) -> int:
+    return int(lib().gdn_attn_decode_workspace_size(
+        n_queries, H_q, H_kv, d, GDN_BF16 if dtype == torch.bfloat16 else GDN_F32))
+
+
+def attn_decode_workspace(n_queries: int, H_q: int, H_kv: int, d: int, dtype=torch.bfloat16,
+                          device="cuda") -> torch.Tensor:
+    """A workspace for gdn_attn_decode and gdn_qsa_attn_decode (any contents)."""
+    n = gdn_attn_decode_workspace_size(n_queries, H_q, H_kv, d, dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _decode_operands(q, q_pos, kv, out, lse, want_lse, workspace):
+    if q.dim() != 4 or q.shape[3] != kv.d:
+        raise ValueError(f"q must be [N, n_queries, H_q, {kv.d}], got {tuple(q.shape)}")
+    N, T, H_q = q.shape[:3]
+    dev = kv.device
+    if N > kv.seqs:
+        raise ValueError(f"page_table has {kv.seqs} rows for {N} sequences")
+    qp = _addr(q, "q", kv.dtype, q.shape, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty(N, T, H_q, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = attn_decode_workspace(T, H_q, kv.H_kv, kv.d, kv.dtype, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return (out, lse, N, T, H_q, qp, _addr(q_pos, "q_pos", torch.int32, (N,), dev),
+            _addr(out, "out", kv.dtype, q.shape, dev),
+            _addr(lse, "lse", torch.float32, (N, T, H_q), dev), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+
+
+@_placed
+def gdn_attn_decode(q, q_pos, kv: PagedKV, *, scale: Optional[float] = None, softcap: float = 0.0,
+                    window: int = 0, out=None, lse=None, want_lse: bool = True, workspace=None):
+    """Attention of the newest tokens over the whole cache: q [N, T, H_q, d] (query j of
+    sequence n at position q_pos[n] + j, seeing the tokens at or before it, with window > 0 only
+    the last `window` of them), q_pos int32 [N].  scale None is d^-0.5; softcap > 0 caps scores
+    by a tanh.  Returns (out, lse [N, T, H_q] float32 or None)."""
+    out, lse, N, T, H_q, qp, pp, op, lp, wp, wn = _decode_operands(q, q_pos, kv, out, lse, want_lse,
+                                                                   workspace)
+    st = lib().gdn_attn_decode(qp, pp, kv.ref, op, lp, N, T, H_q,
+                               kv.d ** -0.5 if scale is None else scale, softcap, window, wp, wn,
+                               _launch_stream(kv))
+    _check(st, "gdn_attn_decode")
+    return out, lse
+
+
+@_placed
+def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
+                        scale: Optional[float] = None, softcap: float = 0.0, out=None, lse=None,
+                        want_lse: bool = True, workspace=None):
+    """Attention of the newest tokens over listed tokens: as gdn_attn_decode, but query j of
+    sequence n sees the tokens that token_idx[n, j] lists (int32 [N, T, L], or [N, L] for T = 1,
+    as gdn_qsa_index_decode and gdn_qsa_index_multi return it; -1 pads) and the newest `recent`
+    ones, each of those once.  Returns (out, lse)."""
+    out, lse, N, T, H_q, qp, pp, op, lp, wp, wn = _decode_operands(q, q_pos, kv, out, lse, want_lse,
+                                                                   workspace)
+    L = token_idx.shape[-1]
+    shape = (N, L) if T == 1 and token_idx.dim() == 2 else (N, T, L)
+    st = lib().gdn_qsa_attn_decode(qp, pp, kv.ref,
+                                   _addr(token_idx, "token_idx", torch.int32, shape, kv.device), L,
+                                   recent, op, lp, N, T, H_q,
+                                   kv.d ** -0.5 if scale is None else scale, softcap, wp, wn,
+                                   _launch_stream(kv))
+    _check(st, "gdn_qsa_attn_decode")
+    return out, lse

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "../../include/attn.h"
 #include "../../include/qsa.h"
 
 #define GDN_API extern "C" __attribute__((visibility("default")))
@@ -51,6 +52,17 @@ cudaError_t launch_qsa_index(const void *q, const int32_t *q_pos, const void *k_
                              int budget, float rope_base, int32_t *block_idx,
                              float *block_score, int32_t *token_idx, void *workspace,
                              cudaStream_t stream);
+cudaError_t launch_kv_append(const gdn_paged_kv &kv, const void *k, const void *v, const void *q,
+                             void *q_out, long long k_stride, long long v_stride,
+                             long long q_stride, const int32_t *cu, const int32_t *pos0,
+                             int num_seqs, long long T_total, int H_q, const float *inv_freq,
+                             int rope_dims, const int32_t *rope_pos, const int32_t *sections,
+                             int n_axes, bool interleaved, cudaStream_t stream);
+size_t attn_decode_workspace_bytes(int rows, int d, int sms);
+cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int32_t *q_pos,
+                               const int32_t *list, int list_len, int recent, bool lists,
+                               void *out, float *lse, int N, int T, int H_q, float scale,
+                               float cap, int window, void *workspace, cudaStream_t stream);
 size_t static_scratch_capacity();
 cudaError_t static_scratch_ptr(void **out);
 }  // namespace gdn
@@ -457,6 +469,143 @@ GDN_API gdn_status gdn_qsa_index_multi(const void *q, const int32_t *q_pos, cons
     return qsa_index(q, q_pos, k_hat, cu_blocks, num_seqs, total_blocks, n_queries,
                      budget_blocks, rope_base, block_idx, block_score, token_idx, workspace,
                      workspace_bytes, stream);
+}
+
+// ------------------------------------------- paged cache and its attention (attn.h)
+namespace {
+constexpr int32_t kMostHeads = 4096;       // keeps every per-token item count inside an int
+
+gdn_status paged_checks(const gdn_paged_kv *kv, int32_t num_seqs)
+{
+    if (!kv || num_seqs < 0) return GDN_ERR_INVALID_ARG;
+    if (kv->dtype != GDN_F32 && kv->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (kv->num_pages < 0 || kv->max_pages < 0 || kv->H_kv <= 0 || kv->d <= 0)
+        return GDN_ERR_INVALID_ARG;
+    if (!head_dim_ok(kv->d) || kv->H_kv > kMostHeads) return GDN_ERR_UNSUPPORTED;
+    if (kv->page_size < 16 || kv->page_size > 1024 || (kv->page_size & (kv->page_size - 1)))
+        return GDN_ERR_UNSUPPORTED;
+    // rows and tokens are 32-bit numbers in the kernels (their byte offsets are 64-bit)
+    if ((int64_t)kv->num_pages * kv->page_size > INT32_MAX ||
+        (int64_t)kv->max_pages * kv->page_size > INT32_MAX)
+        return GDN_ERR_UNSUPPORTED;
+    if (kv->num_pages > 0 && (!kv->k || !kv->v)) return GDN_ERR_INVALID_ARG;
+    if (num_seqs > 0 && kv->max_pages > 0 && !kv->page_table) return GDN_ERR_INVALID_ARG;
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->page_table, 4))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+bool softcap_ok(float cap) { return cap >= 0.f && cap < INFINITY; }
+bool scale_ok(float scale) { return scale > -INFINITY && scale < INFINITY; }
+}  // namespace
+
+GDN_API gdn_status gdn_kv_append(const gdn_paged_kv *kv, const void *k, const void *v,
+                                 const void *q, void *q_out, int64_t k_stride, int64_t v_stride,
+                                 int64_t q_stride, const int32_t *cu_seqlens, const int32_t *pos0,
+                                 int32_t num_seqs, int64_t T_total, int32_t H_q,
+                                 const float *inv_freq, int32_t rope_dims,
+                                 const int32_t *rope_pos, const int32_t *rope_sections,
+                                 int32_t n_axes, uint32_t flags, cudaStream_t stream)
+{
+    const gdn_status st = paged_checks(kv, num_seqs);
+    if (st != GDN_OK) return st;
+    if (T_total < 0 || T_total > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (flags & ~GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
+    if (!cu_seqlens && T_total > 0 && (num_seqs == 0 || T_total % num_seqs != 0))
+        return GDN_ERR_INVALID_ARG;
+    if (rope_dims < 0 || rope_dims > kv->d || rope_dims % 16 != 0) return GDN_ERR_INVALID_ARG;
+    if (n_axes < 1 || n_axes > GDN_ROPE_MAX_AXES) return GDN_ERR_INVALID_ARG;
+    if (n_axes > 1 && (!rope_pos || !rope_sections)) return GDN_ERR_INVALID_ARG;
+    if (rope_sections) {
+        int64_t sum = 0;
+        for (int a = 0; a < n_axes; ++a) {
+            if (rope_sections[a] < 0) return GDN_ERR_INVALID_ARG;
+            sum += rope_sections[a];
+        }
+        if (sum != rope_dims / 2) return GDN_ERR_INVALID_ARG;
+    }
+    if (T_total == 0 || num_seqs == 0) return GDN_OK;
+    if (!k || !v || (q != nullptr) != (q_out != nullptr)) return GDN_ERR_INVALID_ARG;
+    if (q && H_q <= 0) return GDN_ERR_INVALID_ARG;
+    if (q && H_q > kMostHeads) return GDN_ERR_UNSUPPORTED;
+    if (rope_dims > 0 && !inv_freq) return GDN_ERR_INVALID_ARG;
+    const int64_t vec = kv->dtype == GDN_BF16 ? 8 : 4;
+    if (k_stride % vec || v_stride % vec || (q && q_stride % vec)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+        !aligned(cu_seqlens, 4) || !aligned(pos0, 4) || !aligned(inv_freq, 4) ||
+        !aligned(rope_pos, 4))
+        return GDN_ERR_INVALID_ARG;
+    const cudaError_t e = gdn::launch_kv_append(
+        *kv, k, v, q, q_out, k_stride, v_stride, q_stride, cu_seqlens, pos0, num_seqs, T_total,
+        H_q, inv_freq, rope_dims, rope_pos, rope_sections, n_axes,
+        (flags & GDN_ROPE_INTERLEAVED) != 0, stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+GDN_API size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, int32_t H_kv,
+                                              int32_t d, gdn_dtype dtype)
+{
+    if (n_queries < 1 || n_queries > GDN_ATTN_MAX_QUERIES || H_kv <= 0 || H_q <= 0 ||
+        H_q % H_kv != 0 || H_q > kMostHeads || !head_dim_ok(d) ||
+        (dtype != GDN_F32 && dtype != GDN_BF16))
+        return 0;
+    int sms = gdn::device_sm_count();
+    if (sms <= 0) sms = kDefaultSms;
+    return gdn::attn_decode_workspace_bytes(H_q / H_kv * n_queries, d, sms);
+}
+
+namespace {
+gdn_status attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *kv,
+                       const int32_t *list, int32_t list_len, int32_t recent, bool lists,
+                       void *out, float *lse, int32_t num_seqs, int32_t n_queries, int32_t H_q,
+                       float scale, float softcap, int32_t window, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream)
+{
+    const gdn_status st = paged_checks(kv, num_seqs);
+    if (st != GDN_OK) return st;
+    if (n_queries < 1 || n_queries > GDN_ATTN_MAX_QUERIES) return GDN_ERR_UNSUPPORTED;
+    if (H_q <= 0 || H_q % kv->H_kv != 0) return GDN_ERR_INVALID_ARG;
+    if (H_q > kMostHeads) return GDN_ERR_UNSUPPORTED;
+    if (!scale_ok(scale) || !softcap_ok(softcap) || window < 0) return GDN_ERR_INVALID_ARG;
+    if (lists) {
+        if (list_len < 0 || recent < 0) return GDN_ERR_INVALID_ARG;
+        if (list_len > GDN_ATTN_MAX_LIST || recent > 65536) return GDN_ERR_UNSUPPORTED;
+        if (list_len > 0 && num_seqs > 0 && !list) return GDN_ERR_INVALID_ARG;
+        if (!aligned(list, 4)) return GDN_ERR_INVALID_ARG;
+    }
+    if (num_seqs == 0) return GDN_OK;
+    if (!q || !q_pos || !out || !workspace) return GDN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(q_pos, 4) ||
+        !aligned(lse, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (workspace_bytes <
+        gdn_attn_decode_workspace_size(n_queries, H_q, kv->H_kv, kv->d, kv->dtype))
+        return GDN_ERR_INVALID_ARG;
+    const cudaError_t e =
+        gdn::launch_attn_decode(*kv, q, q_pos, list, list_len, recent, lists, out, lse, num_seqs,
+                                n_queries, H_q, scale, softcap, window, workspace, stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+}  // namespace
+
+GDN_API gdn_status gdn_attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *kv,
+                                   void *out, float *lse, int32_t num_seqs, int32_t n_queries,
+                                   int32_t H_q, float scale, float softcap, int32_t window,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    return attn_decode(q, q_pos, kv, nullptr, 0, 0, false, out, lse, num_seqs, n_queries, H_q,
+                       scale, softcap, window, workspace, workspace_bytes, stream);
+}
+
+GDN_API gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos,
+                                       const gdn_paged_kv *kv, const int32_t *token_idx,
+                                       int32_t list_len, int32_t recent, void *out, float *lse,
+                                       int32_t num_seqs, int32_t n_queries, int32_t H_q,
+                                       float scale, float softcap, void *workspace,
+                                       size_t workspace_bytes, cudaStream_t stream)
+{
+    return attn_decode(q, q_pos, kv, token_idx, list_len, recent, true, out, lse, num_seqs,
+                       n_queries, H_q, scale, softcap, 0, workspace, workspace_bytes, stream);
 }
 
 GDN_API const char *gdn_status_string(gdn_status status)

@@ -1,0 +1,745 @@
+// gdn_attn_decode and gdn_qsa_attn_decode (include/attn.h): attention of the newest tokens of
+// every sequence over the paged cache, whole or by lists.
+//
+//   out = sum_t e^{x_t - m} v_t / sum_t e^{x_t - m},  m = max_t x_t,  x_t = cap(scale q . k_t)
+//
+// in one pass over the keys with a running m and sum; parts of a sequence that different CTAs
+// (or warps) ran are joined by out = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i.
+//
+// Every visible key and value is read once for all the query rows that share it (the heads of
+// its group, and the drafted tokens when no lists are given), so the calls are bound by HBM:
+// per key and head 4 d bytes (bf16) against at most 4 d flops per query row.
+//
+//  - Work split.  A unit is one (sequence, key head[, row block][, drafted token]); its keys are
+//    cut into steps of 64.  The steps of all units form one line, and each CTA takes an equal
+//    stretch of it, wherever units begin and end: ragged lengths cost nothing, one long
+//    sequence uses every SM, and no length is needed on the host (a captured graph stays valid
+//    as sequences grow).  A unit that lies in one CTA is finished there; the parts of the
+//    others go to the workspace (at most two per CTA) and attn_join_kernel joins them.
+//  - bf16: a warp owns 16 query rows as one mma.sync m16n8k16 row tile.  With few rows the
+//    product is far from the tensor pipe's limit, so what counts is that loads never pause:
+//    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
+//    private ring of cp.async stages and waits for nobody else.
+//  - fp32: the same skeleton with fp32 FMAs (1e-4 rules out reduced-precision operands).
+#include <math.h>
+#include <stdint.h>
+
+#include "device_once.h"
+#include "paged_kv.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStep = 64;                  // keys per step of a CTA, 16 per warp
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 2;
+constexpr int kLoadRows = 16;              // keys one warp loads per step
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// What CTA c leaves for the join: the unit that began in it and ends in a later CTA.
+struct JoinRecord {
+    int n, sub;                            // sequence; unit within the sequence
+    int parts;                             // CTAs c .. c + parts - 1 hold a part (0: none)
+    int first_slot;                        // where CTA c's own part is (later ones: slot 0)
+};
+
+struct DecodeParams {
+    PagedView cache;
+    const void *q;
+    const int32_t *q_pos, *list;
+    void *out;
+    float *lse;
+    float *part_o;                         // [grid, 2, rows, D]
+    float2 *part_ml;                       // [grid, 2, rows]
+    JoinRecord *rec;                       // [grid]
+    int N, T, H_q, G;                      // G = H_q / H_kv
+    int rows, row_blocks;                  // query rows of a unit (before blocking), blocks
+    int units_per_seq;
+    int list_len, recent, window;
+    float scale, cap;                      // score multiplier; 0: no cap
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes global -> shared; reads nothing and writes zeros when !live
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Scores in the base-2 domain: log2(e) times the scaled, capped score.  tanh(y) is written
+// 1 - 2 / (1 + e^{2y}): its absolute error stays at a few 2^-24 of the cap.
+__device__ __forceinline__ float score2(float dot, float scale, float cap) {
+    if (cap == 0.f) return dot * (scale * kLog2e);
+    const float e = ex2(dot * scale * (2.f * kLog2e / cap));
+    return cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+}
+
+// --------------------------------------------------------------------- where the work is
+// Keys that unit (n, sub) walks: dense, tokens [lo, hi) with lo on a step; lists, positions
+// of list (padded to a step) and newest tokens.
+struct Span {
+    long long lo;                          // dense: first token of step 0
+    int steps;
+};
+
+template <bool LIST>
+__device__ __forceinline__ Span span_of(const DecodeParams &p, int n) {
+    Span s;
+    if (LIST) {
+        s.lo = 0;
+        s.steps = (p.list_len + kStep - 1) / kStep + (p.recent + kStep - 1) / kStep;
+    } else {
+        const long long pos = __ldg(p.q_pos + n);
+        long long hi = pos + p.T;                                // one past the last query
+        const long long cap = cache_capacity(p.cache);
+        hi = hi < cap ? hi : cap;
+        s.lo = p.window > 0 && pos - p.window + 1 > 0 ? (pos - p.window + 1) / kStep * kStep : 0;
+        s.steps = hi > s.lo ? (int)((hi - s.lo + kStep - 1) / kStep) : 0;
+    }
+    if (s.steps < 1) s.steps = 1;          // a unit that sees nothing still writes its zeros
+    return s;
+}
+
+struct Unit {
+    int n, sub;                            // sequence, unit within it
+    int h, rb, j;                          // key head, row block, drafted token (lists)
+};
+template <bool LIST>
+__device__ __forceinline__ Unit unit_of(const DecodeParams &p, int n, int sub) {
+    Unit u;
+    u.n = n;
+    u.sub = sub;
+    u.rb = sub % p.row_blocks;
+    u.h = sub / p.row_blocks % p.cache.H_kv;
+    u.j = LIST ? sub / (p.row_blocks * p.cache.H_kv) : 0;
+    return u;
+}
+// (token, head) of row r of a unit
+template <bool LIST>
+__device__ __forceinline__ size_t row_head(const DecodeParams &p, const Unit &u, int r) {
+    const int j = LIST ? u.j : r / p.G, g = LIST ? r : r % p.G;
+    return ((size_t)u.n * p.T + j) * p.H_q + (size_t)u.h * p.G + g;
+}
+
+// ------------------------------------------------------------------------------- loading
+// One warp's 16 keys of one step into its 16 rows of a stage (rows of D elements, 16-byte
+// chunk c of row r at c ^ (r & 7)), keys at kdst, values at vdst; returns the mask of keys that
+// are present.  Absent keys are zero-filled, so nothing a dead row holds reaches a product.
+template <typename E, int D, bool LIST>
+__device__ __forceinline__ uint32_t load_keys(const DecodeParams &p, const Unit &u, const Span &sp,
+                                              long long pos, int step, int sub, uint32_t kdst,
+                                              uint32_t vdst) {
+    constexpr int CH = D * (int)sizeof(E) / 16, RPI = 32 / CH, ITER = kLoadRows / RPI;
+    const int lane = threadIdx.x & 31, key = lane & 15;
+    int row;                               // cache row of key `key`
+    if (LIST) {
+        const int i = step * kStep + sub * kLoadRows + key;
+        const int list_pad = (p.list_len + kStep - 1) / kStep * kStep;
+        const long long at = pos + u.j;
+        long long t = -1;
+        if (i < list_pad) {
+            if (i < p.list_len) {
+                t = __ldg(p.list + ((size_t)u.n * p.T + u.j) * p.list_len + i);
+                if (t > at - p.recent) t = -1;
+            }
+        } else if (i - list_pad < p.recent) {
+            t = at - p.recent + 1 + (i - list_pad);
+        }
+        row = cache_row(p.cache, u.n, t);
+    } else {
+        const long long t = sp.lo + (long long)step * kStep + sub * kLoadRows + key;
+        row = t < pos + p.T ? cache_row(p.cache, u.n, t) : -1;
+    }
+    const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+    const int c = lane % CH;
+    const size_t pitch = (size_t)p.cache.H_kv * D * sizeof(E);
+    const size_t off = (size_t)u.h * D * sizeof(E) + (size_t)c * 16;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int r = lane / CH + i * RPI;
+        const int at = __shfl_sync(0xffffffffu, row, r);
+        const size_t src = (size_t)(at < 0 ? 0 : at) * pitch + off;
+        const uint32_t d = (uint32_t)(r * CH + (c ^ (r & 7))) * 16;
+        cp_async16(kdst + d, p.cache.k + src, at >= 0);
+        cp_async16(vdst + d, p.cache.v + src, at >= 0);
+    }
+    return present;
+}
+
+// ------------------------------------------------------------------- bf16: tensor cores
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A warp's 16 query rows against the keys of its team.  Lane (g = lane / 4, c = lane % 4) holds
+// rows g and g + 8: scores of keys 8 i + 2 c, + 1; outputs of dims 8 i + 2 c, + 1.
+template <int D, int TEAM, bool LIST>
+struct TensorRows {
+    using E = __nv_bfloat16;
+    static constexpr int kTeam = TEAM, kRows = 16 * TEAM;        // rows of a unit's block
+    static constexpr int kTileKeys = 16 * TEAM;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+    int first[2], last[2];                 // tokens row g / g + 8 may see (dense)
+
+    __device__ void begin(const DecodeParams &p, const Unit &u, long long pos, float *) {
+        const int lane = threadIdx.x & 31, wt = (threadIdx.x >> 5) % TEAM;
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = u.rb * kRows + wt * 16 + g + 8 * e;
+            const bool live = r < p.rows;
+            const E *src = static_cast<const E *>(p.q) + row_head<LIST>(p, u, live ? r : 0) * D + 2 * c;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                q[k][e] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * k)) : 0u;
+                q[k][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * k + 8)) : 0u;
+            }
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+            const long long at = pos + (LIST || !live ? 0 : r / p.G);
+            last[e] = LIST ? INT32_MAX : (int)(at < INT32_MAX ? at : INT32_MAX);
+            first[e] = LIST || p.window <= 0 ? INT32_MIN
+                       : (int)(at - p.window + 1 > INT32_MIN ? at - p.window + 1 : INT32_MIN);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+
+    // kt, vt: the team's tile of kTileKeys rows; token0: token of its key 0 (dense)
+    __device__ __forceinline__ void tile(const DecodeParams &p, uint32_t kt, uint32_t vt,
+                                         uint64_t present, long long token0, float *) {
+        constexpr int NT = kTileKeys / 8;
+        const int lane = threadIdx.x & 31, c = lane & 3;
+        float s[NT][4];
+        const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+            const int r = 16 * i + kr;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                ldsm4(kt + (uint32_t)(r * (D / 8) + ((2 * k + kc) ^ (r & 7))) * 16, b);
+                mma16816(s[2 * i], q[k], b[0], b[1]);
+                mma16816(s[2 * i + 1], q[k], b[2], b[3]);
+            }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 8 * i + 2 * c + (e & 1);
+                bool live = (present >> key) & 1;
+                if (!LIST) {
+                    const int t = (int)(token0 + key);
+                    live = live && t <= last[e >> 1] && t >= first[e >> 1];
+                }
+                s[i][e] = live ? score2(s[i][e], p.scale, p.cap) : -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], s[i][e]);
+            }
+        float shift[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            mx[e] = fmaxf(mx[e], m[e]);
+            shift[e] = mx[e] == -INFINITY ? 0.f : mx[e];
+            const float f = ex2(m[e] - shift[e]);               // 0 while m is -inf
+            m[e] = mx[e];
+            l[e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) { o[i][2 * e] *= f; o[i][2 * e + 1] *= f; }
+        }
+        // rounded to bf16 for the product (each weight is off by half a step, 2^-8 of itself, at
+        // most; over many keys the errors average out below the output's own rounding); the sum
+        // takes the unrounded weights, so lse is exact to fp32
+        uint32_t w[NT / 2][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float a = ex2(s[i][2 * e] - shift[e]), b = ex2(s[i][2 * e + 1] - shift[e]);
+                l[e] += a + b;
+                w[i >> 1][(i & 1) * 2 + e] = pack2(a, b);
+            }
+        const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < NT / 2; ++k) {
+            const int r = 16 * k + vr;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t b[4];
+                ldsm4t(vt + (uint32_t)(r * (D / 8) + ((2 * i + vc) ^ (r & 7))) * 16, b);
+                mma16816(o[2 * i], w[k], b[0], b[1]);
+                mma16816(o[2 * i + 1], w[k], b[2], b[3]);
+            }
+        }
+    }
+
+    // this warp's part: rows at so[kRows][D], maxima and sums at sml[kRows]
+    __device__ void put(float *so, float2 *sml) {
+        const int lane = threadIdx.x & 31, wt = (threadIdx.x >> 5) % TEAM;
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = wt * 16 + g + 8 * e;
+            float sum = l[e];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (c == 0) sml[r] = make_float2(m[e], sum);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2 *>(so + r * D + 8 * i + 2 * c) =
+                    make_float2(o[i][2 * e], o[i][2 * e + 1]);
+        }
+    }
+};
+
+// --------------------------------------------------------------------- fp32: CUDA cores
+// A warp's 16 keys against R query rows held in shared memory.  Scores: lane pair (key, half of
+// the dims); weights go through shared memory; outputs: lane owns D / 32 dims of every row.
+template <int D, int R, bool LIST>
+struct FmaRows {
+    using E = float;
+    static constexpr int kTeam = 1, kRows = R, kTileKeys = 16, kV = D / 32;
+    float o[R][kV];
+    float m[R], l[R];
+    long long pos0;
+    int row0;
+
+    // shared: q [R][D], then per warp weights [R][16]
+    __device__ void begin(const DecodeParams &p, const Unit &u, long long pos, float *shared) {
+        for (int i = threadIdx.x; i < R * D; i += kThreads) {
+            const int r = u.rb * R + i / D;
+            shared[i] = r < p.rows ? __ldg(static_cast<const float *>(p.q) +
+                                           row_head<LIST>(p, u, r) * D + i % D) : 0.f;
+        }
+        pos0 = pos;
+        row0 = u.rb * R;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) o[r][e] = 0.f;
+        }
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ void tile(const DecodeParams &p, uint32_t kt, uint32_t vt,
+                                         uint64_t present, long long token0, float *shared) {
+        constexpr int CH = D / 4;
+        const int lane = threadIdx.x & 31, key = lane >> 1, half = lane & 1;
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < CH / 2; ++c) {
+            const int ch = 2 * c + half;                        // the pair reads neighbours
+            float4 k;
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+                         : "r"(kt + (uint32_t)(key * CH + (ch ^ (key & 7))) * 16) : "memory");
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 q = *reinterpret_cast<const float4 *>(shared + r * D + ch * 4);
+                s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+            }
+        }
+        float *w = shared + R * D + (threadIdx.x >> 5) * R * 16;
+        const long long t = token0 + key;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+            bool live = (present >> key) & 1;
+            if (!LIST) {
+                const long long at = pos0 + (row0 + r) / p.G;
+                live = live && t <= at && (p.window <= 0 || t > at - p.window);
+            }
+            const float x = live ? score2(s[r], p.scale, p.cap) : -INFINITY;
+            float mx = x;
+#pragma unroll
+            for (int d = 2; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            mx = fmaxf(mx, m[r]);
+            const float shift = mx == -INFINITY ? 0.f : mx;
+            const float f = ex2(m[r] - shift), e = ex2(x - shift);
+            m[r] = mx;
+            l[r] = l[r] * f + (half ? 0.f : e);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) o[r][v] *= f;
+            if (half == 0) w[r * 16 + key] = e;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            float v[kV];
+            const uint32_t at = vt + (uint32_t)(k * CH + ((lane * kV >> 2) ^ (k & 7))) * 16;
+            if constexpr (kV == 4)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at) : "memory");
+            else
+                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                             : "=f"(v[0]), "=f"(v[1]) : "r"(at + (lane & 1) * 8) : "memory");
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float x = w[r * 16 + k];
+#pragma unroll
+                for (int e = 0; e < kV; ++e) o[r][e] = fmaf(x, v[e], o[r][e]);
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ void put(float *so, float2 *sml) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float sum = warp_sum(l[r]);
+            if (lane == 0) sml[r] = make_float2(m[r], sum);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) so[r * D + lane * kV + e] = o[r][e];
+        }
+    }
+};
+
+// -------------------------------------------------------------------------------- kernel
+template <class ROWS, int D>
+struct Layout {
+    static constexpr int kTeams = kWarps / ROWS::kTeam;
+    static constexpr int kRowBytes = D * (int)sizeof(typename ROWS::E);
+    static constexpr int kStageBytes = kStep * kRowBytes;              // K or V of one step
+    static constexpr int kRing = kStages * 2 * kStageBytes;
+    // the join of the CTA's teams reuses the ring
+    static constexpr int kJoin = kTeams * ROWS::kRows * (D + 2) * 4;
+    static constexpr int kExtra = sizeof(typename ROWS::E) == 4 ? (ROWS::kRows * D + kWarps * ROWS::kRows * 16) * 4 : 0;
+    static constexpr int kMask = kStages * kWarps * 4;
+    static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kSmem = kBody + kExtra + kMask + 64;
+};
+
+template <typename E> __device__ __forceinline__ void store2(void *p, size_t i, float a, float b);
+template <> __device__ __forceinline__ void store2<float>(void *p, size_t i, float a, float b) {
+    *reinterpret_cast<float2 *>(static_cast<float *>(p) + i) = make_float2(a, b);
+}
+template <> __device__ __forceinline__ void store2<__nv_bfloat16>(void *p, size_t i, float a, float b) {
+    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + i) = pack2(a, b);
+}
+
+template <int TEAM> __device__ __forceinline__ void team_sync() {
+    if (TEAM == 1) __syncwarp();
+    else if (TEAM == kWarps) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)(threadIdx.x >> 5) / TEAM), "n"(32 * TEAM) : "memory");
+}
+
+// First step of CTA c's stretch when G CTAs share W steps, and the CTA that runs step x.
+__device__ __forceinline__ long long stretch(long long W, int G, int c) { return W * c / G; }
+__device__ __forceinline__ int cta_of(long long W, int G, long long x) {
+    return (int)(((x + 1) * G + W - 1) / W) - 1;
+}
+
+template <class ROWS, int D, bool LIST>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+    using E = typename ROWS::E;
+    using L = Layout<ROWS, D>;
+    constexpr int TEAM = ROWS::kTeam;
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ long long scan[kThreads];
+    __shared__ long long found[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *extra = reinterpret_cast<float *>(sm + L::kBody);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(sm + L::kBody + L::kExtra);   // [stage][warp]
+
+    pdl_trigger();
+    // all steps, and where this CTA's stretch begins: thread t sums sequences [t per, t per + per)
+    const int per = (p.N + kThreads - 1) / kThreads;
+    const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    long long mine = 0;
+    for (int n = n0; n < n1; ++n) mine += (long long)span_of<LIST>(p, n).steps * p.units_per_seq;
+    scan[tid] = mine;
+    __syncthreads();
+    for (int d = 1; d < kThreads; d <<= 1) {
+        const long long x = tid >= d ? scan[tid - d] : 0;
+        __syncthreads();
+        scan[tid] += x;
+        __syncthreads();
+    }
+    const long long W = scan[kThreads - 1];
+    const int G = (int)(W < (long long)gridDim.x ? W : gridDim.x);
+    const int cta = blockIdx.x;
+    if (tid == 0) p.rec[cta].parts = 0;
+    if (cta >= G) return;
+    const long long begin = stretch(W, G, cta), end = stretch(W, G, cta + 1);
+    const long long before = scan[tid] - mine;
+    if (before <= begin && begin < scan[tid]) {
+        long long at = before;
+        for (int n = n0; n < n1; ++n) {
+            const long long x = (long long)span_of<LIST>(p, n).steps * p.units_per_seq;
+            if (begin < at + x) { found[0] = n; found[1] = begin - at; break; }
+            at += x;
+        }
+    }
+    __syncthreads();
+    int n = (int)found[0];
+    Span sp = span_of<LIST>(p, n);
+    int sub = (int)(found[1] / sp.steps), step = (int)(found[1] % sp.steps);
+
+    ROWS rows;
+    const int team = warp / TEAM;
+    const uint32_t ring = smem_addr(sm);
+    for (long long at = begin; at < end;) {
+        const Unit u = unit_of<LIST>(p, n, sub);
+        const long long pos = __ldg(p.q_pos + n);
+        const int count = (int)min((long long)(sp.steps - step), end - at);
+        auto load = [&](int i) {
+            if (i < count) {
+                const int st = i % kStages;
+                const uint32_t dst = ring + st * 2 * L::kStageBytes + warp * kLoadRows * L::kRowBytes;
+                const uint32_t m = load_keys<E, D, LIST>(p, u, sp, pos, step + i, warp, dst,
+                                                         dst + L::kStageBytes);
+                if (lane == 0) masks[st * kWarps + warp] = m;
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i);
+        rows.begin(p, u, pos, extra);
+        for (int i = 0; i < count; ++i) {
+            cp_wait<kStages - 2>();
+            team_sync<TEAM>();             // the tile is there, and the slot of tile i - 1 is free
+            load(i + kStages - 1);
+            const int st = i % kStages;
+            uint64_t present = 0;
+#pragma unroll
+            for (int w = 0; w < TEAM; ++w)
+                present |= (uint64_t)masks[st * kWarps + team * TEAM + w] << (16 * w);
+            const uint32_t kt = ring + st * 2 * L::kStageBytes + team * ROWS::kTileKeys * L::kRowBytes;
+            rows.tile(p, kt, kt + L::kStageBytes, present,
+                      sp.lo + (long long)(step + i) * kStep + team * ROWS::kTileKeys, extra);
+        }
+        cp_wait<0>();
+        __syncthreads();                   // the ring is free: join the teams in it
+        float *so = reinterpret_cast<float *>(sm);
+        float2 *sml = reinterpret_cast<float2 *>(so + L::kTeams * ROWS::kRows * D);
+        rows.put(so + team * ROWS::kRows * D, sml + team * ROWS::kRows);
+        __syncthreads();
+        const bool whole = count == sp.steps;
+        const int slot = at == begin ? 0 : 1;
+        const int live_rows = min(ROWS::kRows, p.rows - u.rb * ROWS::kRows);
+        for (int i = tid; i < live_rows * (D / 2); i += kThreads) {
+            const int r = i / (D / 2), c = 2 * (i % (D / 2));
+            float m = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < L::kTeams; ++t) m = fmaxf(m, sml[t * ROWS::kRows + r].x);
+            const float shift = m == -INFINITY ? 0.f : m;
+            float l = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+            for (int t = 0; t < L::kTeams; ++t) {
+                const float2 ml = sml[t * ROWS::kRows + r];
+                const float f = ex2(ml.x - shift);
+                const float2 x = *reinterpret_cast<const float2 *>(so + (t * ROWS::kRows + r) * D + c);
+                l = fmaf(ml.y, f, l);
+                a = fmaf(x.x, f, a);
+                b = fmaf(x.y, f, b);
+            }
+            if (whole) {
+                const size_t rh = row_head<LIST>(p, u, u.rb * ROWS::kRows + r);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                store2<E>(p.out, rh * D + c, a * inv, b * inv);
+                if (c == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                const size_t pr = ((size_t)cta * 2 + slot) * ROWS::kRows + r;
+                *reinterpret_cast<float2 *>(p.part_o + pr * D + c) = make_float2(a, b);
+                if (c == 0) p.part_ml[pr] = make_float2(m, l);
+            }
+        }
+        if (step == 0 && !whole && tid == 0) {
+            JoinRecord r;
+            r.n = n;
+            r.sub = sub;
+            r.parts = cta_of(W, G, at + sp.steps - 1) - cta + 1;
+            r.first_slot = slot;
+            p.rec[cta] = r;
+        }
+        at += count;
+        step = 0;
+        if (at < end && ++sub == p.units_per_seq) {
+            sub = 0;
+            sp = span_of<LIST>(p, ++n);
+        }
+        __syncthreads();                   // the next unit loads into the ring
+    }
+}
+
+// Joins the parts of the units that more than one CTA ran: CTA (c, r) of this grid joins row r
+// of the unit that began in CTA c, its warps taking the parts in turn.
+constexpr int kJoinWarps = 8;
+
+template <typename E, int D, int ROWS, bool LIST>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ DecodeParams p) {
+    __shared__ float so[kJoinWarps][D];
+    __shared__ float2 sml[kJoinWarps];
+    const int c = blockIdx.x, r = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int V = D / 32;
+    pdl_wait();
+    const JoinRecord rec = p.rec[c];
+    if (rec.parts < 2) return;
+    const Unit u = unit_of<LIST>(p, rec.n, rec.sub);
+    const int row = u.rb * ROWS + r;
+    if (row >= p.rows) return;
+    float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < rec.parts; i += kJoinWarps) {
+        const size_t at = ((size_t)(c + i) * 2 + (i == 0 ? rec.first_slot : 0)) * ROWS + r;
+        const float2 ml = p.part_ml[at];
+        const float *src = p.part_o + at * D + lane * V;
+        const float mx = fmaxf(m, ml.x), shift = mx == -INFINITY ? 0.f : mx;
+        const float f = ex2(m - shift), g = ex2(ml.x - shift);
+        l = l * f + ml.y * g;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = o[e] * f + src[e] * g;
+        m = mx;
+    }
+    if (lane == 0) sml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sml[w].x);
+    const float shift = m == -INFINITY ? 0.f : m;
+    const int col = 2 * threadIdx.x;
+    float a = 0.f, b = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(sml[w].x - shift);
+        l = fmaf(sml[w].y, f, l);
+        a = fmaf(so[w][col], f, a);
+        b = fmaf(so[w][col + 1], f, b);
+    }
+    const size_t rh = row_head<LIST>(p, u, row);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    store2<E>(p.out, rh * D + col, a * inv, b * inv);
+    if (threadIdx.x == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <class ROWS, int D, bool LIST> PerDevice g_setup;
+
+template <class ROWS, int D, bool LIST>
+cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
+    constexpr int smem = Layout<ROWS, D>::kSmem;
+    int sms = 0;
+    cudaError_t e = g_setup<ROWS, D, LIST>.ensure([] {
+        return cudaFuncSetAttribute(attn_decode_kernel<ROWS, D, LIST>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    }, &sms);
+    if (e != cudaSuccess) return e;
+    const int grid = sms * kCtasPerSm;
+    p.row_blocks = (p.rows + ROWS::kRows - 1) / ROWS::kRows;
+    p.units_per_seq = p.cache.H_kv * p.row_blocks * (LIST ? p.T : 1);
+    p.rec = static_cast<JoinRecord *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.rec + grid);
+    p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)grid * 2 * ROWS::kRows);
+    attn_decode_kernel<ROWS, D, LIST><<<grid, kThreads, smem, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, p.rows < ROWS::kRows ? p.rows : ROWS::kRows);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<typename ROWS::E, D, ROWS::kRows, LIST>, p);
+}
+
+template <int D, bool LIST>
+cudaError_t launch_dim(const DecodeParams &p, bool bf16, void *ws, cudaStream_t stream) {
+    if (bf16) {
+        if (p.rows <= 16) return launch_rows<TensorRows<D, 1, LIST>, D, LIST>(p, ws, stream);
+        if (p.rows <= 32) return launch_rows<TensorRows<D, 2, LIST>, D, LIST>(p, ws, stream);
+        return launch_rows<TensorRows<D, 4, LIST>, D, LIST>(p, ws, stream);
+    }
+    if (p.rows == 1) return launch_rows<FmaRows<D, 1, LIST>, D, LIST>(p, ws, stream);
+    if (p.rows <= 4) return launch_rows<FmaRows<D, 4, LIST>, D, LIST>(p, ws, stream);
+    return launch_rows<FmaRows<D, 8, LIST>, D, LIST>(p, ws, stream);
+}
+
+constexpr int kMostRows = 64;              // largest ROWS::kRows
+
+}  // namespace
+
+// `rows`: query rows that share a key head (H_q / H_kv x n_queries), blocked as launch_dim does
+size_t attn_decode_workspace_bytes(int rows, int d, int sms) {
+    const size_t block = rows <= 16 ? 16 : rows <= 32 ? 32 : kMostRows;
+    return (size_t)sms * kCtasPerSm *
+           (sizeof(JoinRecord) + 2 * block * (sizeof(float2) + d * sizeof(float)));
+}
+
+cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int32_t *q_pos,
+                               const int32_t *list, int list_len, int recent, bool lists,
+                               void *out, float *lse, int N, int T, int H_q, float scale,
+                               float cap, int window, void *workspace, cudaStream_t stream) {
+    DecodeParams p = {};
+    p.cache = paged_view(kv);
+    p.q = q;
+    p.q_pos = q_pos;
+    p.list = list;
+    p.out = out;
+    p.lse = lse;
+    p.N = N;
+    p.T = T;
+    p.H_q = H_q;
+    p.G = H_q / kv.H_kv;
+    p.rows = lists ? p.G : p.G * T;
+    p.list_len = list_len;
+    p.recent = recent;
+    p.window = window;
+    p.scale = scale;
+    p.cap = cap;
+    const bool bf16 = kv.dtype == GDN_BF16;
+    if (kv.d == 128)
+        return lists ? launch_dim<128, true>(p, bf16, workspace, stream)
+                     : launch_dim<128, false>(p, bf16, workspace, stream);
+    return lists ? launch_dim<64, true>(p, bf16, workspace, stream)
+                 : launch_dim<64, false>(p, bf16, workspace, stream);
+}
+
+}  // namespace gdn
