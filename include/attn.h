@@ -11,6 +11,7 @@
  *                        sequence over its whole cache;
  *   gdn_qsa_attn_decode  the same over the token lists of gdn_qsa_index_decode / _multi and
  *                        the newest tokens;
+ *   gdn_attn_prefill     attention of prompts (packed, each behind tokens cached earlier).
  *
  * With p the position of a query, h its head and h' = h / (H_q / H_kv) its key head:
  *
@@ -121,6 +122,26 @@ gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos, const gdn_pa
                                void *out, float *lse, int32_t num_seqs, int32_t n_queries,
                                int32_t H_q, float scale, float softcap, void *workspace,
                                size_t workspace_bytes, cudaStream_t stream);
+
+/* Prompts.  Query i of sequence n sits at position p = pos0[n] + i; with e = pos0[n] plus the
+ * sequence's tokens in this call, it sees the tokens 0 <= t < e with t <= p, with window > 0
+ * only those with t > p - window, and with prefix_len those with t < prefix_len[n] too (a
+ * prefix that is seen both ways).
+ *   q, out     : [T_total, H_q, d]; rows from cu_seqlens[num_seqs] on are left alone
+ *   cu_seqlens : DEVICE int32[num_seqs + 1], or NULL for num_seqs sequences of
+ *                T_total / num_seqs tokens each
+ *   pos0       : DEVICE int32[num_seqs] tokens cached before this call (>= 0), or NULL for 0
+ *   prefix_len : DEVICE int32[num_seqs] or NULL; GDN_ERR_UNSUPPORTED together with a window
+ *   lse        : [T_total, H_q] fp32 or NULL
+ *   workspace  : at least 16 bytes of device memory whose first 16 hold the device error
+ *                word (zero-filled before first use; gdn_get_device_error reads it), or NULL:
+ *                a device-side timeout is then not reported.
+ * Keys and values of the call's own tokens are in the cache already. */
+gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv, const int32_t *cu_seqlens,
+                            const int32_t *pos0, const int32_t *prefix_len, void *out,
+                            float *lse, int32_t num_seqs, int64_t T_total, int32_t H_q,
+                            float scale, float softcap, int32_t window, void *workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,7 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_decode_step",
             "gdn_qsa_index_multi_workspace_size", "gdn_qsa_index_multi",
             "gdn_set_wait_budget", "gdn_set_prefill_segment_tokens", "gdn_prefill_schedule",
             "gdn_kv_append", "gdn_attn_decode_workspace_size", "gdn_attn_decode",
-            "gdn_qsa_attn_decode")
+            "gdn_qsa_attn_decode", "gdn_attn_prefill")
 
 _lib = None
 
@@ -114,6 +114,8 @@ def lib():
         L.gdn_qsa_attn_decode.argtypes = [P, P, KV, P, I32, I32, P, P, I32, I32, I32, F, F, P, SZ,
                                           P]
         L.gdn_qsa_attn_decode.restype = ctypes.c_int
+        L.gdn_attn_prefill.argtypes = [P, KV, P, P, P, P, P, I32, I64, I32, F, F, I32, P, SZ, P]
+        L.gdn_attn_prefill.restype = ctypes.c_int
         L.gdn_get_device_error.argtypes = [P, P]
         L.gdn_get_device_error.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
@@ -733,4 +735,40 @@ def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
                                    kv.d ** -0.5 if scale is None else scale, softcap, wp, wn,
                                    _launch_stream(kv))
     _check(st, "gdn_qsa_attn_decode")
+    return out, lse
+
+
+@_placed
+def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=None,
+                     scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, out=None,
+                     lse=None, want_lse: bool = True, workspace=None):
+    """Attention of prompts whose keys and values are in the cache already: q [T_total, H_q, d]
+    with cu_seqlens int32 [N + 1], or [B, T, H_q, d]; query i of sequence n sits at position
+    pos0[n] + i (pos0 None: 0) and sees the tokens at or before it, with window > 0 only the last
+    `window` of them, with prefix_len int32 [N] also those before prefix_len[n].  A workspace (16
+    zero-filled bytes or more) records a device-side timeout for gdn_get_device_error.  Returns
+    (out, lse [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are
+    left alone."""
+    T_total, N = _sequences(q, cu_seqlens, kv)
+    if q.shape[-1] != kv.d:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected head dim {kv.d}")
+    dev, H_q = kv.device, q.shape[-2]
+    qp = _addr(q, "q", kv.dtype, q.shape, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib().gdn_attn_prefill(
+        qp, kv.ref, _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev),
+        _addr(pos0, "pos0", torch.int32, (N,), dev),
+        _addr(prefix_len, "prefix_len", torch.int32, (N,), dev),
+        _addr(out, "out", kv.dtype, q.shape, dev),
+        _addr(lse, "lse", torch.float32, q.shape[:-1], dev), N, T_total, H_q,
+        kv.d ** -0.5 if scale is None else scale, softcap, window, wp, wn, _launch_stream(kv))
+    _check(st, "gdn_attn_prefill")
     return out, lse

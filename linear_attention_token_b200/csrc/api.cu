@@ -63,6 +63,10 @@ cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int3
                                const int32_t *list, int list_len, int recent, bool lists,
                                void *out, float *lse, int N, int T, int H_q, float scale,
                                float cap, int window, void *workspace, cudaStream_t stream);
+cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
+                                const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
+                                int N, long long T_total, int H_q, float scale, float cap,
+                                int window, void *workspace, uint32_t budget, cudaStream_t stream);
 size_t static_scratch_capacity();
 cudaError_t static_scratch_ptr(void **out);
 }  // namespace gdn
@@ -479,7 +483,7 @@ gdn_status paged_checks(const gdn_paged_kv *kv, int32_t num_seqs)
 {
     if (!kv || num_seqs < 0) return GDN_ERR_INVALID_ARG;
     if (kv->dtype != GDN_F32 && kv->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
-    if (kv->num_pages < 0 || kv->max_pages < 0 || kv->H_kv <= 0 || kv->d <= 0)
+    if (kv->num_pages <= 0 || kv->max_pages < 0 || kv->H_kv <= 0 || kv->d <= 0)
         return GDN_ERR_INVALID_ARG;
     if (!head_dim_ok(kv->d) || kv->H_kv > kMostHeads) return GDN_ERR_UNSUPPORTED;
     if (kv->page_size < 16 || kv->page_size > 1024 || (kv->page_size & (kv->page_size - 1)))
@@ -488,7 +492,7 @@ gdn_status paged_checks(const gdn_paged_kv *kv, int32_t num_seqs)
     if ((int64_t)kv->num_pages * kv->page_size > INT32_MAX ||
         (int64_t)kv->max_pages * kv->page_size > INT32_MAX)
         return GDN_ERR_UNSUPPORTED;
-    if (kv->num_pages > 0 && (!kv->k || !kv->v)) return GDN_ERR_INVALID_ARG;
+    if (!kv->k || !kv->v) return GDN_ERR_INVALID_ARG;
     if (num_seqs > 0 && kv->max_pages > 0 && !kv->page_table) return GDN_ERR_INVALID_ARG;
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->page_table, 4))
         return GDN_ERR_INVALID_ARG;
@@ -606,6 +610,34 @@ GDN_API gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos,
 {
     return attn_decode(q, q_pos, kv, token_idx, list_len, recent, true, out, lse, num_seqs,
                        n_queries, H_q, scale, softcap, 0, workspace, workspace_bytes, stream);
+}
+
+GDN_API gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv,
+                                    const int32_t *cu_seqlens, const int32_t *pos0,
+                                    const int32_t *prefix_len, void *out, float *lse,
+                                    int32_t num_seqs, int64_t T_total, int32_t H_q, float scale,
+                                    float softcap, int32_t window, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream)
+{
+    const gdn_status st = paged_checks(kv, num_seqs);
+    if (st != GDN_OK) return st;
+    if (T_total < 0 || T_total > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (!cu_seqlens && T_total > 0 && (num_seqs == 0 || T_total % num_seqs != 0))
+        return GDN_ERR_INVALID_ARG;
+    if (H_q <= 0 || H_q % kv->H_kv != 0) return GDN_ERR_INVALID_ARG;
+    if (H_q > kMostHeads) return GDN_ERR_UNSUPPORTED;
+    if (!scale_ok(scale) || !softcap_ok(softcap) || window < 0) return GDN_ERR_INVALID_ARG;
+    if (window > 0 && prefix_len) return GDN_ERR_UNSUPPORTED;
+    if (T_total == 0 || num_seqs == 0) return GDN_OK;
+    if (!q || !out) return GDN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 4) || !aligned(pos0, 4) ||
+        !aligned(prefix_len, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return GDN_ERR_INVALID_ARG;
+    if (workspace && workspace_bytes < sizeof(gdn::DeviceError)) return GDN_ERR_INVALID_ARG;
+    const cudaError_t e = gdn::launch_attn_prefill(*kv, q, cu_seqlens, pos0, prefix_len, out, lse,
+                                                   num_seqs, T_total, H_q, scale, softcap, window,
+                                                   workspace, g_wait_budget.load(), stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 GDN_API const char *gdn_status_string(gdn_status status)

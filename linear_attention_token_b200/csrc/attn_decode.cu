@@ -159,7 +159,9 @@ __device__ __forceinline__ uint32_t load_keys(const DecodeParams &p, const Unit 
         row = cache_row(p.cache, u.n, t);
     } else {
         const long long t = sp.lo + (long long)step * kStep + sub * kLoadRows + key;
-        row = t < pos + p.T ? cache_row(p.cache, u.n, t) : -1;
+        // what no query sees is not read: it may hold anything
+        const bool seen = t < pos + p.T && (p.window <= 0 || t > pos - p.window);
+        row = seen ? cache_row(p.cache, u.n, t) : -1;
     }
     const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
     const int c = lane % CH;

@@ -1,0 +1,504 @@
+// gdn_attn_prefill (include/attn.h), bf16: attention of prompts over the paged cache on the
+// tcgen05 tensor cores.
+//
+//   S = Q K^T,  x = cap(scale S),  m = running row maximum,  P = e^{x - m},
+//   O <- O e^{m_old - m} + P V,  l <- l e^{m_old - m} + sum P,   out = O / l
+//
+// A CTA owns 256 query rows that share one key head: the tokens of a block, each with `pack`
+// heads (a power of two that divides the group), so a K / V tile in shared memory serves all of
+// them and the causal edge of the block is 256 / pack tokens wide.  Rows form two tiles of 128
+// whose products and exponentials alternate:
+//
+//   tensor:   S_A(j+1)  PV_B(j)  S_B(j+1)  PV_A(j+1)  ...
+//   warps:    softmax B(j)       softmax A(j+1)       ...
+//
+// Per pair of 128 x 128 tiles (d = 128) the tensor pipe needs 2048 cycles and the 2 x 16384
+// exponentials, at 16 per cycle and SM, 2048 as well: the two are balanced, and what is lost is
+// what does not overlap.
+//  - warps 0-3, 4-7: the softmax of tile A, B; a thread owns a row (TMEM lane), so maxima and
+//    sums need no exchange.  P goes back to TMEM over the first half of S, as the A operand of PV.
+//    O is rescaled only when a row's maximum grew by more than 2^8 (until then P and l simply use
+//    the old one): after the first tiles that is rare, so no warps are kept for it.
+//  - warp 8: issues the products.  PV(j) and S(j+1) of a tile go out together; S(j+1) overwrites
+//    the columns P(j) was in, after PV(j) read them (one thread's products run in order).
+//  - warp 9 (10 and 11 only fill their warpgroup): loads.  K and V tiles of 128 tokens alternate through a ring, gathered page by page
+//    with TMA; tokens that are absent are left out of the softmax by a mask, and their V rows (and
+//    those past the sequence) are zeroed, so nothing a dead row holds reaches a product.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "attn_prefill.cuh"
+#include "device_once.h"
+#include "sm100.cuh"
+
+namespace gdn {
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 384, kSlots = 4, kMaskRing = 8;
+// Registers a thread: 168 at launch (384 threads); the softmax warps, which hold a row of scores,
+// take what the third warpgroup gives up: 2 x 208 + 88 = 3 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kTile = 128;                 // query rows of a tile, tokens of a K / V tile
+constexpr uint32_t kPollNs = 2000, kDrainBudget = GDN_DEFAULT_WAIT_BUDGET;
+constexpr float kLazy = 8.f;               // growth of a row maximum (base 2) that O may lag
+
+enum Bar {
+    B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2,
+    B_O = B_P + 2, B_FIX = B_O + 2, B_DRAIN, B_COUNT
+};
+
+template <int D>
+struct Smem {
+    static constexpr uint32_t kHalf = kTile * 128;             // 64 dims of a tile
+    static constexpr uint32_t kTileBytes = (D / 64) * kHalf;
+    static constexpr uint32_t kQ = 0, kRing = 2 * kTileBytes;
+    static constexpr uint32_t kMask = kRing + kSlots * kTileBytes;
+    static constexpr uint32_t kBars = kMask + kMaskRing * 16;
+    static constexpr uint32_t kMisc = kBars + 8 * ((B_COUNT + 1) / 2 * 2);
+    static constexpr uint32_t kTotal = kMisc + 16 + 1024;       // 1024: alignment of the base
+};
+constexpr uint32_t kTmS = 0, kTmO = 256;                        // TMEM columns, 128 per tile each
+
+template <int N> __device__ __forceinline__ void regs_take() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_give() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uint32_t budget,
+                                          const volatile int *abort_flag) {
+    for (uint32_t i = 0; i < budget; ++i) {
+        if (mbar_try_wait_sleep(bar, parity, kPollNs)) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ AttnPrefillParams p) {
+    using L = Smem<D>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int bt_tile = kTile >> p.pack_shift, bt = 2 * bt_tile;        // tokens of a tile, block
+    int n, blk;
+    if (!find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; }, blockIdx.x, n, blk))
+        return;
+    const int packs = p.G >> p.pack_shift;
+    const int hk = blockIdx.y / packs;                                   // key head
+    const int h0 = hk * p.G + (blockIdx.y % packs << p.pack_shift);      // first query head
+    const Tokens seq = sequence_of(p, n);
+    const long long first = seq.first;
+    const int len = seq.len;
+    const Sight see(p, n, len);
+    const int e = see.e;
+    const int q0 = blk * bt;
+    const int k_lo = see.lo(q0), k_base = k_lo / kTile * kTile;          // oldest token seen, its tile
+    int tiles[2];                                                        // K / V tiles each row tile walks
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int a = q0 + i * bt_tile;
+        const int last = min(a + bt_tile, len) - 1;
+        const int hi = a < len ? see.hi(last) : 0;
+        tiles[i] = hi > k_base ? (hi - k_base + kTile - 1) / kTile : 0;
+    }
+    const int nt = max(tiles[0], tiles[1]);
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
+    if (warp == 8) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    if (tid == 0) {
+        for (int b = 0; b < B_COUNT; ++b) mbar_init(bars + b, b == B_P || b == B_P + 1 ? 128 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](int b, int k) -> bool {                              // k-th completion of barrier b
+        return wait_bounded(bars + b, (uint32_t)(k & 1), p.budget, abort_flag);
+    };
+    auto fail = [&](int where) {
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            record_error(p.err, GDN_ERR_TIMEOUT, where);
+        }
+    };
+
+    if (warp < 8) {
+        // ==================================================================== softmax
+        regs_take<kRegsSoftmax>();
+        const int i = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_at = tmem + lanes + kTmS + 128 * i, o_at = tmem + lanes + kTmO + 128 * i;
+        const int tok = q0 + i * bt_tile + (row >> p.pack_shift);
+        const int head = h0 + (row & ((1 << p.pack_shift) - 1));
+        const int lo = see.lo(tok), hi = see.hi(tok);
+        // tiles that every row of this row tile sees whole
+        const int lo_max = see.lo(q0 + (i + 1) * bt_tile - 1), hi_min = see.hi(q0 + i * bt_tile);
+        float m = -INFINITY, l = 0.f;                                    // m in base-2 units
+        bool ok = true;
+        const float k2 = CAP ? p.scale * (2.f * kLog2e / p.cap) : p.scale2;
+        const float cap2 = p.cap * kLog2e;
+#pragma unroll 1
+        for (int j = 0; j < tiles[i]; ++j) {
+            if (!__all_sync(0xffffffffu, wait(B_S + i, j))) { fail(1 + i); ok = false; break; }
+            tc_fence_after();
+            uint32_t raw[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, raw[c]);
+            const int k0 = k_base + j * kTile;
+            const uint4 pm = *reinterpret_cast<const uint4 *>(sm + L::kMask + (j % kMaskRing) * 16);
+            tmem_wait_ld();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 128; ++c) {
+                const float x = __uint_as_float(raw[c >> 5][c & 31]);
+                s[c] = CAP ? capped2(x, k2, cap2) : x;
+            }
+            const bool whole = k0 >= lo_max && k0 + kTile <= hi_min &&
+                               (pm.x & pm.y & pm.z & pm.w) == 0xffffffffu;
+            if (!whole) {
+                const uint32_t pw[4] = {pm.x, pm.y, pm.z, pm.w};
+                const int a = lo - k0, z = hi - k0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    // bits of tokens [a, z) of this word
+                    const int b0 = min(max(a - 32 * w, 0), 32), b1 = min(max(z - 32 * w, 0), 32);
+                    const uint32_t below1 = b1 == 32 ? 0xffffffffu : (1u << b1) - 1u;
+                    const uint32_t below0 = b0 == 32 ? 0xffffffffu : (1u << b0) - 1u;
+                    const uint32_t live = pw[w] & below1 & ~below0;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        s[32 * w + c] = (live >> c) & 1 ? s[32 * w + c] : -INFINITY;
+                }
+            }
+            float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 128; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            if (!CAP && mx != -INFINITY) mx *= k2;
+            const bool grow = mx > m + kLazy;                            // also when m is -inf
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? ex2(m - mx) : 1.f;                // 0 from -inf
+                if (grow) m = mx;
+                l *= f;
+                if (j > 0) {
+                    // PV(j - 1) is complete: S(j) was issued after it and has arrived
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st32(o_at + 32 * c, o);
+                    }
+                }
+            }
+            const float shift = m == -INFINITY ? 0.f : m;
+            // each weight is rounded to bf16 for the product (off by 2^-8 of itself at most);
+            // the sum takes the unrounded ones
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const int at = 64 * c + 2 * x;
+                    const float a = CAP ? ex2(s[at] - shift) : ex2(fmaf(s[at], k2, -shift));
+                    const float b = CAP ? ex2(s[at + 1] - shift) : ex2(fmaf(s[at + 1], k2, -shift));
+                    sum[0] += a;
+                    sum[1] += b;
+                    w[x] = pack2(a, b);
+                }
+                tmem_st32(s_at + 32 * c, w);
+            }
+            l += sum[0] + sum[1];
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive_local(bars + B_P + i);
+        }
+        if (ok && tiles[i] > 0 && !__all_sync(0xffffffffu, wait(B_O + i, 0))) {
+            fail(3 + i);
+            ok = false;
+        }
+        if (ok) {
+            tc_fence_after();
+            // a thread's row: D values, in pieces of 32 (the TMEM loads are warp-wide)
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t rh = (size_t)(first + tok) * p.H_q + head;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + rh * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (tiles[i] > 0) {
+                    tmem_ld32(o_at + 32 * c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = 0;
+                }
+                if (tok < len) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = pack2(__uint_as_float(o[8 * x + 2 * y]) * inv,
+                                         __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (p.lse && tok < len) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+    } else {
+        regs_give<kRegsOther>();
+        if (warp == 8) {
+        // =================================================================== products
+        if (lane == 0 && nt > 0) {
+            const uint32_t neg = p.scale < 0.f && !CAP ? 1u << 14 : 0u;  // scale2 is |scale|
+            const uint32_t id_s = idesc_bf16(128, 128, false, false) | neg;
+            const uint32_t id_o = idesc_bf16(128, D, false, true);
+            const uint32_t ring = smem_u32(sm + L::kRing), qs = smem_u32(sm + L::kQ);
+            auto scores = [&](int i, int j) {
+                const uint32_t kt = ring + (2 * j % kSlots) * L::kTileBytes;
+                const uint32_t qt = qs + i * L::kTileBytes;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
+                    umma_bf16(tmem + kTmS + 128 * i, sdesc_kmajor(qt + off), sdesc_kmajor(kt + off), id_s, ks > 0);
+                }
+            };
+            bool ok = wait(B_Q, 0) && wait(B_FULL, 0);
+            int issued = 0;
+            if (ok) {
+                tc_fence_after();
+                for (int i = 0; i < 2; ++i)
+                    if (tiles[i] > 0) { scores(i, 0); umma_commit(bars + B_S + i); issued = 1; }
+                umma_commit(bars + B_EMPTY + 0);
+            }
+#pragma unroll 1
+            for (int j = 0; ok && j < nt; ++j) {
+                const int vs = (2 * j + 1) % kSlots;
+                ok = wait(B_FULL + vs, (2 * j + 1) / kSlots);
+                if (ok && j + 1 < nt) ok = wait(B_FULL + (2 * j + 2) % kSlots, (2 * j + 2) / kSlots);
+                if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; ok && i < 2; ++i) {
+                    if (j >= tiles[i]) continue;
+                    if (!(ok = wait(B_P + i, j))) break;
+                    tc_fence_after();
+                    const uint32_t vt = ring + vs * L::kTileBytes;
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        umma_bf16_ta(tmem + kTmO + 128 * i, tmem + kTmS + 128 * i + 8 * ks,
+                                     sdesc_mnmajor(vt + ks * 2048, L::kHalf), id_o, j > 0 || ks > 0);
+                    if (j + 1 < tiles[i]) {
+                        scores(i, j + 1);
+                        umma_commit(bars + B_S + i);
+                    } else {
+                        umma_commit(bars + B_O + i);
+                    }
+                }
+                if (!ok) break;
+                umma_commit(bars + B_EMPTY + vs);
+                if (j + 1 < nt) umma_commit(bars + B_EMPTY + (2 * j + 2) % kSlots);
+            }
+            if (!ok) {
+                fail(5);
+                if (issued) {                                            // let the products end first
+                    umma_commit(bars + B_DRAIN);
+                    mbar_wait(bars + B_DRAIN, 0, kDrainBudget);
+                }
+            }
+        }
+        __syncwarp();
+        } else if (warp == 9) {
+        // ====================================================================== loads
+        const int ps = 1 << p.cache.page_shift, box = ps < kTile ? ps : kTile;
+        const int boxes = kTile / box;
+        if (nt > 0) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bars + B_Q, 2 * L::kTileBytes);
+                for (int i = 0; i < 2; ++i)
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_3d(sm + L::kQ + i * L::kTileBytes + h * L::kHalf, &tm_q, bars + B_Q,
+                                    64 * h, h0, (int)(first + q0 + i * bt_tile));
+            }
+            bool ok = true;
+            int done = 0, fixes = 0;                                     // slots handed on; V tiles patched
+            bool patching = false;
+#pragma unroll 1
+            for (int j = 0; ok && j < nt; ++j) {
+                const int k0 = k_base + j * kTile;
+                const int t = k0 + lane * box;
+                const int src = lane < boxes && t < e ? cache_row(p.cache, n, t) : -1;
+                const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
+                const uint32_t bytes = __popc(there) * box * D * 2;
+                const bool patch = __popc(there) < boxes || k0 + kTile > e || k0 < k_lo;
+                if (lane < 4) {
+                    // presence, 32 tokens a word (a box is at least 16 tokens)
+                    const uint32_t a = (there >> (32 * lane / box)) & 1, b = (there >> ((32 * lane + 16) / box)) & 1;
+                    reinterpret_cast<uint32_t *>(sm + L::kMask + (j % kMaskRing) * 16)[lane] =
+                        (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
+                }
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int use = 2 * j + v, slot = use % kSlots;
+                    unsigned char *dst = sm + L::kRing + slot * L::kTileBytes;
+                    if (use >= kSlots) ok = wait(B_EMPTY + slot, use / kSlots - 1);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    const bool fix = v && patch;
+                    uint64_t *bar = bars + (fix ? B_FIX : B_FULL + slot);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (src >= 0)
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(dst + h * L::kHalf + lane * box * 128, v ? &tm_v : &tm_k, bar,
+                                        64 * h, hk, src);
+                    if (fix) {
+                        patching = true;
+                        ok = wait(B_FIX, fixes);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        patching = false;
+                        ++fixes;
+                        for (int r = lane; r < kTile; r += 32)
+                            if (k0 + r >= e || k0 + r < k_lo || !((there >> (r / box)) & 1))
+                                for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c)
+                                        *reinterpret_cast<uint4 *>(dst + h * L::kHalf + r * 128 + 16 * c) =
+                                            make_uint4(0, 0, 0, 0);
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_local(bars + B_FULL + slot);
+                    }
+                    ++done;
+                }
+            }
+            if (!ok) {
+                if (lane == 0) fail(6);
+                __syncwarp();
+            }
+            if (*abort_flag) {
+                // let this CTA's copies land before its shared memory is released
+                mbar_wait(bars + B_Q, 0, kDrainBudget);
+                if (patching) mbar_wait(bars + B_FIX, (uint32_t)(fixes & 1), kDrainBudget);
+                for (int s = max(0, done - kSlots); s < done; ++s)
+                    mbar_wait(bars + B_FULL + s % kSlots, (uint32_t)(s / kSlots & 1), kDrainBudget);
+            }
+        }
+        __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult r;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// [rows, heads, d] bf16, boxes of 64 dims x box_heads x box_rows in the 128-byte swizzle
+bool make_map(CUtensorMap *map, const void *base, long long rows, int heads, int d, int box_heads,
+              int box_rows) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool CAP> PerDevice g_setup;
+
+template <int D, bool CAP>
+cudaError_t launch_tc(const AttnPrefillParams &p, const gdn_paged_kv &kv, cudaStream_t stream) {
+    constexpr int smem = Smem<D>::kTotal;
+    cudaError_t e = g_setup<D, CAP>.ensure([] {
+        return cudaFuncSetAttribute(attn_prefill_kernel<D, CAP>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    const int pack = 1 << p.pack_shift, bt = 2 * (kTile >> p.pack_shift);
+    const int box = kv.page_size < kTile ? kv.page_size : kTile;
+    const long long rows = (long long)kv.num_pages * kv.page_size;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, p.q, p.T_total, p.H_q, D, pack, kTile / pack) ||
+        !make_map(&mk, kv.k, rows, kv.H_kv, D, 1, box) ||
+        !make_map(&mv, kv.v, rows, kv.H_kv, D, 1, box))
+        return cudaErrorInvalidValue;
+    // at most one block per sequence is not full
+    const long long blocks = p.cu ? p.T_total / bt + p.N : (p.T_seq + bt - 1) / bt * p.N;
+    attn_prefill_kernel<D, CAP><<<dim3((unsigned)blocks, (unsigned)(kv.H_kv * (p.G >> p.pack_shift))),
+                                  kThreads, smem, stream>>>(mq, mk, mv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill_f32(const AttnPrefillParams &p, int d, cudaStream_t stream);
+
+cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
+                                const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
+                                int N, long long T_total, int H_q, float scale, float cap,
+                                int window, void *workspace, uint32_t budget, cudaStream_t stream) {
+    AttnPrefillParams p = {};
+    p.cache = paged_view(kv);
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.cu = cu;
+    p.pos0 = pos0;
+    p.prefix = prefix;
+    p.T_total = T_total;
+    p.T_seq = cu ? 0 : T_total / N;
+    p.N = N;
+    p.H_q = H_q;
+    p.G = H_q / kv.H_kv;
+    p.window = window;
+    // heads packed into a row tile: the largest power of two, up to 16, that divides the group
+    while (p.pack_shift < 4 && p.G % (2 << p.pack_shift) == 0) ++p.pack_shift;
+    p.scale = scale;
+    // a scale of 0 makes every score equal; so does 1e-30, and -inf (a masked score) times it is
+    // still -inf
+    p.scale2 = fmaxf(fabsf(scale) * kLog2e, 1e-30f);
+    p.cap = cap;
+    p.err = static_cast<DeviceError *>(workspace);
+    p.budget = budget;
+    if (kv.dtype == GDN_F32) return launch_attn_prefill_f32(p, kv.d, stream);
+    if (kv.d == 128)
+        return cap > 0.f ? launch_tc<128, true>(p, kv, stream) : launch_tc<128, false>(p, kv, stream);
+    return cap > 0.f ? launch_tc<64, true>(p, kv, stream) : launch_tc<64, false>(p, kv, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,128 @@
+// What the two gdn_attn_prefill kernels share: the call's parameters, the sequences' tokens, what
+// a query sees, and the scores' scaling.
+#pragma once
+
+#include <math.h>
+
+#include "paged_kv.cuh"
+
+namespace gdn {
+
+struct AttnPrefillParams {
+    PagedView cache;
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *cu, *pos0, *prefix;
+    long long T_total, T_seq;              // T_seq: tokens per sequence when cu is null
+    int N, H_q, G, window;
+    int pack_shift;                        // rows of a tile: token r >> pack_shift, head the rest
+    float scale2, cap;                     // |scale| log2 e; 0: no cap
+    float scale;
+    DeviceError *err;
+    uint32_t budget;
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Tokens {
+    long long first;                       // row of the sequence's first token in q, out
+    int len;
+};
+// Tokens of sequence n, inside the call's T_total whatever the offsets say.
+__device__ __forceinline__ Tokens sequence_of(const AttnPrefillParams &p, int n) {
+    Tokens t;
+    if (!p.cu) {
+        t.first = n * p.T_seq;
+        t.len = (int)p.T_seq;
+        return t;
+    }
+    t.first = __ldg(p.cu + n);
+    const long long end = min((long long)__ldg(p.cu + n + 1), p.T_total);
+    t.len = t.first >= 0 && end > t.first ? (int)(end - t.first) : 0;
+    return t;
+}
+
+// What the queries of sequence n see: query i sees the tokens [lo(i), hi(i)), both growing with i.
+struct Sight {
+    long long start;
+    int e, pre, window;
+    __device__ __forceinline__ Sight(const AttnPrefillParams &p, int n, int len) {
+        start = p.pos0 ? __ldg(p.pos0 + n) : 0;
+        e = (int)min(max(start + len, 0LL), cache_capacity(p.cache));
+        pre = p.prefix ? min(__ldg(p.prefix + n), e) : 0;
+        window = p.window;
+    }
+    __device__ __forceinline__ int hi(int i) const {
+        return (int)max(min(start + i + 1, (long long)e), (long long)pre);
+    }
+    __device__ __forceinline__ int lo(int i) const {
+        return window > 0 ? (int)min(max(start + i - window + 1, 0LL), (long long)e) : 0;
+    }
+};
+
+// Block x of the call: sequence n and its block b.  blocks_of(len) is a sequence's number of
+// blocks; they are numbered from the last one back, since a sequence's last blocks see the most
+// tokens and should start first.  All THREADS threads call it; false when x is past the last.
+template <int THREADS, class F>
+__device__ __forceinline__ bool find_block(const AttnPrefillParams &p, F &&blocks_of, long long x,
+                                           int &n, int &b) {
+    __shared__ int sums[THREADS / 32], found[2];
+    if (!p.cu) {
+        const long long at = blocks_of(p.T_seq) * p.N - 1 - x;
+        if (at < 0) return false;
+        b = (int)(at / p.N);               // the last blocks of all sequences first
+        n = (int)(at % p.N);
+        return true;
+    }
+    // thread t counts the blocks of sequences [t per, t per + per)
+    const int tid = threadIdx.x, per = (p.N + THREADS - 1) / THREADS;
+    const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    const int lane = tid & 31, warp = tid >> 5;
+    int mine = 0;
+    for (int i = n0; i < n1; ++i) mine += (int)blocks_of(sequence_of(p, i).len);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sums[warp] = inc;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int before = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const int at = (int)(total - 1 - x);
+    if (at >= before && at < before + mine) {
+        int left = at - before;
+        for (int i = n0; i < n1; ++i) {
+            const int nb = (int)blocks_of(sequence_of(p, i).len);
+            if (left < nb) { found[0] = i; found[1] = left; break; }
+            left -= nb;
+        }
+    }
+    __syncthreads();
+    n = found[0];
+    b = found[1];
+    return n >= 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// log2(e) cap tanh(dot scale / cap), with tanh(y) = 1 - 2 / (1 + e^{2y})
+__device__ __forceinline__ float capped2(float dot, float k, float cap2) {
+    return cap2 * (1.f - __fdividef(2.f, 1.f + ex2(dot * k)));
+}
+
+}  // namespace gdn

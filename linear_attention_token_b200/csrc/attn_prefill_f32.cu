@@ -1,0 +1,189 @@
+// gdn_attn_prefill (include/attn.h), fp32: the same attention on the CUDA cores, since operands of
+// fewer bits would not hold fp32's tolerance.
+//
+// A CTA owns 64 query rows of one key head (row r of a sequence: token r / G, head r % G of the
+// group) and walks the tokens they see in tiles of 64, with a running maximum and sum.  Thread
+// (ty, tx) of 16 x 16 holds the scores of rows 4 ty + a and keys tx + 16 b, and the outputs of the
+// same rows and D / 16 dims, so a row's maxima and sums stay inside a half warp.  Both products
+// run from shared memory at four FMAs per 16-byte operand load or better: FMA-bound.
+#include <stdint.h>
+
+#include "attn_prefill.cuh"
+#include "device_once.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256, kRows = 64, kKeys = 64;
+
+template <int D>
+struct Smem {
+    static constexpr int kPitch = D + 4;                     // rows of Q and K: no bank conflicts
+    static constexpr int kQ = 0, kK = kQ + kRows * kPitch, kV = kK + kKeys * kPitch,
+                         kP = kV + kKeys * D, kRow = kP + kRows * (kKeys + 4);
+    static constexpr int kBytes = (kRow + kKeys) * 4;
+};
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
+    using L = Smem<D>;
+    extern __shared__ float sm[];
+    float *sq = sm + L::kQ, *sk = sm + L::kK, *sv = sm + L::kV, *sp = sm + L::kP;
+    int *rows = reinterpret_cast<int *>(sm + L::kRow);       // cache row of each key, -1 absent
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    int n, blk;
+    if (!find_block<kThreads>(p, [&](long long len) { return (len * p.G + kRows - 1) / kRows; },
+                              blockIdx.x, n, blk))
+        return;
+    const int hk = blockIdx.y;
+    const Tokens seq = sequence_of(p, n);
+    const Sight see(p, n, seq.len);
+    const long long r0 = (long long)blk * kRows, r_end = (long long)seq.len * p.G;
+    const int t_first = (int)(r0 / p.G), t_last = (int)((min(r0 + kRows, r_end) - 1) / p.G);
+    const int k_lo = see.lo(t_first), k_hi = see.hi(t_last);
+    auto row_at = [&](long long r) -> size_t {
+        return (size_t)(seq.first + r / p.G) * p.H_q + (size_t)hk * p.G + r % p.G;
+    };
+    constexpr int C4 = D / 4;
+    for (int i = tid; i < kRows * C4; i += kThreads) {
+        const long long r = r0 + i / C4;
+        const float4 x = r < r_end ? __ldg(reinterpret_cast<const float4 *>(p.q) + row_at(r) * C4 + i % C4)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(sq + (i / C4) * L::kPitch + 4 * (i % C4)) = x;
+    }
+    int lo[4], hi[4];
+    float m[4], l[4], o[4][D / 16];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const long long r = r0 + 4 * ty + a;
+        const int t = (int)(min(r, r_end - 1) / p.G);
+        lo[a] = see.lo(t);
+        hi[a] = see.hi(t);
+        m[a] = -INFINITY;
+        l[a] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[a][d] = 0.f;
+    }
+    const float k2 = p.cap > 0.f ? p.scale * (2.f * kLog2e / p.cap) : p.scale * kLog2e;
+    const float cap2 = p.cap * kLog2e;
+    const float *kc = reinterpret_cast<const float *>(p.cache.k), *vc = reinterpret_cast<const float *>(p.cache.v);
+    for (int k0 = k_lo; k0 < k_hi; k0 += kKeys) {
+        __syncthreads();                                     // the last tile has been used
+        if (tid < kKeys) rows[tid] = k0 + tid < k_hi ? cache_row(p.cache, n, k0 + tid) : -1;
+        __syncthreads();
+        for (int i = tid; i < kKeys * C4; i += kThreads) {
+            const int key = i / C4, c = i % C4, row = rows[key];
+            const size_t at = ((size_t)(row < 0 ? 0 : row) * p.cache.H_kv + hk) * C4 + c;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(sk + key * L::kPitch + 4 * c) =
+                row < 0 ? zero : reinterpret_cast<const float4 *>(kc)[at];
+            *reinterpret_cast<float4 *>(sv + key * D + 4 * c) =
+                row < 0 ? zero : reinterpret_cast<const float4 *>(vc)[at];
+        }
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int c = 0; c < C4; ++c) {
+            float4 q[4], k[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) q[a] = *reinterpret_cast<const float4 *>(sq + (4 * ty + a) * L::kPitch + 4 * c);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) k[b] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * b) * L::kPitch + 4 * c);
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) s[a][b] = dot4(q[a], k[b], s[a][b]);
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float mx = m[a];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int key = tx + 16 * b;
+                const bool live = k0 + key >= lo[a] && k0 + key < hi[a] && rows[key] >= 0;
+                s[a][b] = !live ? -INFINITY : p.cap > 0.f ? capped2(s[a][b], k2, cap2) : s[a][b] * k2;
+                mx = fmaxf(mx, s[a][b]);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float shift = mx == -INFINITY ? 0.f : mx, f = ex2(m[a] - shift);
+            m[a] = mx;
+            l[a] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) o[a][d] *= f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float w = ex2(s[a][b] - shift);
+                l[a] += w;
+                sp[(4 * ty + a) * (kKeys + 4) + tx + 16 * b] = w;
+            }
+        }
+        __syncwarp();                                        // a half warp's rows are its own
+#pragma unroll 2
+        for (int k = 0; k < kKeys; k += 4) {
+            float w[4][4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const float4 x = *reinterpret_cast<const float4 *>(sp + (4 * ty + a) * (kKeys + 4) + k);
+                w[a][0] = x.x; w[a][1] = x.y; w[a][2] = x.z; w[a][3] = x.w;
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sv + (k + b) * D + 64 * d + 4 * tx);
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        o[a][4 * d] = fmaf(w[a][b], v.x, o[a][4 * d]);
+                        o[a][4 * d + 1] = fmaf(w[a][b], v.y, o[a][4 * d + 1]);
+                        o[a][4 * d + 2] = fmaf(w[a][b], v.z, o[a][4 * d + 2]);
+                        o[a][4 * d + 3] = fmaf(w[a][b], v.w, o[a][4 * d + 3]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        float sum = l[a];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const long long r = r0 + 4 * ty + a;
+        if (r >= r_end) continue;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const size_t at = row_at(r);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + 64 * d + 4 * tx) =
+                make_float4(o[a][4 * d] * inv, o[a][4 * d + 1] * inv, o[a][4 * d + 2] * inv, o[a][4 * d + 3] * inv);
+        if (tx == 0 && p.lse) p.lse[at] = sum > 0.f ? (m[a] + log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+template <int D> PerDevice g_setup;
+
+template <int D>
+cudaError_t launch_dim(const AttnPrefillParams &p, cudaStream_t stream) {
+    const cudaError_t e = g_setup<D>.ensure([] {
+        return cudaFuncSetAttribute(attn_prefill_f32_kernel<D>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    });
+    if (e != cudaSuccess) return e;
+    const long long blocks = p.cu ? p.T_total * p.G / kRows + p.N : (p.T_seq * p.G + kRows - 1) / kRows * p.N;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    attn_prefill_f32_kernel<D><<<dim3((unsigned)blocks, (unsigned)p.cache.H_kv), kThreads,
+                                 Smem<D>::kBytes, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill_f32(const AttnPrefillParams &p, int d, cudaStream_t stream) {
+    return d == 128 ? launch_dim<128>(p, stream) : launch_dim<64>(p, stream);
+}
+
+}  // namespace gdn

@@ -120,6 +120,33 @@ def test_decode_workspace_size(L):
     assert gdn.gdn_attn_decode_workspace_size(1, 4, 2, 96) == 0
 
 
+def prefill(L, **over):
+    kv, over = paged(**over)
+    a = dict(q=A, cu=None, pos0=None, prefix=None, out=A, lse=None, num_seqs=2, T=64, H_q=4, scale=1.0,
+             cap=0.0, window=0, ws=None, ws_bytes=0)
+    a.update(over)
+    return L.gdn_attn_prefill(P(a["q"]), kv, P(a["cu"]), P(a["pos0"]), P(a["prefix"]), P(a["out"]),
+                              P(a["lse"]), a["num_seqs"], a["T"], a["H_q"], a["scale"], a["cap"],
+                              a["window"], P(a["ws"]), a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("over,expect", PAGED + [
+    (dict(T=-1), BAD), (dict(T=1 << 31), BAD), (dict(T=65), BAD), (dict(num_seqs=0), BAD),
+    (dict(H_q=3), BAD), (dict(H_q=0), BAD), (dict(H_q=8192), UNSUPPORTED),
+    (dict(scale=float("nan")), BAD), (dict(cap=-1.0), BAD), (dict(cap=float("inf")), BAD),
+    (dict(window=-1), BAD), (dict(window=8, prefix=A), UNSUPPORTED), (dict(q=None), BAD),
+    (dict(q=A + 2), BAD), (dict(out=None), BAD), (dict(cu=A + 2), BAD), (dict(pos0=A + 2), BAD),
+    (dict(prefix=A + 2), BAD), (dict(lse=A + 2), BAD), (dict(ws=A, ws_bytes=8), BAD),
+    (dict(ws=A + 8, ws_bytes=64), BAD)])
+def test_prefill_rejects(L, over, expect):
+    assert prefill(L, **over) == expect
+
+
+def test_prefill_nothing_to_do(L):
+    assert prefill(L, T=0, q=None, out=None) == gdn.GDN_OK
+    assert prefill(L, T=0, num_seqs=0) == gdn.GDN_OK
+
+
 # --------------------------------------------------------------------------- the binding
 def _kv(dtype=torch.bfloat16, N=2):
     k = torch.zeros(4, 16, 2, 64, dtype=dtype)
@@ -174,3 +201,22 @@ def test_decode_binding_refusals():
                              ((torch.zeros(3, 1, 4, 64, dtype=bf), pos, kv), ValueError, "rows for 3")):
         with pytest.raises(exc, match=match):
             gdn.gdn_attn_decode(*args, workspace=ws)
+
+
+def test_prefill_binding_refusals():
+    kv, i32, bf = _kv(), torch.int32, torch.bfloat16
+    q, cu = torch.zeros(6, 4, 64, dtype=bf), torch.tensor([0, 2, 6], dtype=i32)
+    for over, exc, match in (
+            (dict(), ValueError, "no CPU path"), (dict(cu_seqlens=cu.long()), TypeError, "int32"),
+            (dict(cu_seqlens=torch.zeros(4, dtype=i32)), ValueError, "page_table has 2 rows"),
+            (dict(pos0=torch.zeros(3, dtype=i32)), ValueError, "pos0"),
+            (dict(prefix_len=torch.zeros(2)), TypeError, "prefix_len"),
+            (dict(out=torch.zeros(6, 4, 64)), TypeError, "out"),
+            (dict(lse=torch.zeros(6, 3)), ValueError, "lse"),
+            (dict(workspace=torch.zeros(64, device="meta")), ValueError, "workspace")):
+        with pytest.raises(exc, match=match):
+            gdn.gdn_attn_prefill(q, kv, **{**dict(cu_seqlens=cu), **over})
+    with pytest.raises(ValueError, match="head dim"):
+        gdn.gdn_attn_prefill(q[..., :32].contiguous(), kv, cu)
+    with pytest.raises(ValueError, match="contiguous"):
+        gdn.gdn_attn_prefill(q.transpose(0, 1).contiguous().transpose(0, 1), kv, cu)
