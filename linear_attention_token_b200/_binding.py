@@ -504,8 +504,8 @@ class PagedKV:
     the library reads; their contents may change at any time, the tensors themselves may not
     (make another PagedKV for another table)."""
 
-    __slots__ = ("k", "v", "page_table", "dtype", "device", "H_kv", "d", "seqs", "code", "ref",
-                 "_struct")
+    __slots__ = ("k", "v", "page_table", "dtype", "device", "index", "H_kv", "d", "seqs", "code",
+                 "ref", "_struct")
 
     def __init__(self, k, v, page_table):
         code = _dtype_code(k)
@@ -525,7 +525,7 @@ class PagedKV:
             if t.device != k.device:
                 raise ValueError(f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.page_table = k, v, page_table
-        self.dtype, self.device, self.code = k.dtype, k.device, code
+        self.dtype, self.device, self.index, self.code = k.dtype, k.device, k.get_device(), code
         num_pages, page_size, self.H_kv, self.d = k.shape
         self.seqs = page_table.shape[0]
         self._struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), num_pages,
@@ -535,9 +535,9 @@ class PagedKV:
 
 def _launch_stream(kv) -> int:
     """The current stream; every operand was found on the cache's device before."""
-    if kv.device.type != "cuda":
+    if kv.index < 0:
         raise ValueError("the cache must be in CUDA tensors (libgdn has no CPU path)")
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(kv.index)
 
 
 def _placed(fn):
@@ -545,51 +545,56 @@ def _placed(fn):
     current, so that what the call allocates belongs to the stream it is used on."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if first.is_cuda:
+        index = first.get_device()
+        if index >= 0:
             if stream is not None:
-                if stream.device != first.device:
+                if stream.device.index != index:
                     raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
                 with torch.cuda.stream(stream):
                     return fn(first, *args, **kw)
-            if first.device.index != torch.cuda.current_device():
-                with torch.cuda.device(first.device):
+            if index != torch._C._cuda_getDevice():
+                with torch.cuda.device(index):
                     return fn(first, *args, **kw)
         return fn(first, *args, **kw)
     return call
 
 
-def _addr(t, name, dtype, shape, dev):
+def _addr(t, name, dtype, shape, kv):
     """Device address of an operand (None stays None) after checking type, shape, layout and
-    device."""
+    device.  (These checks run on every call of small kernels: one compare each.)"""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if t.get_device() != kv.index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {kv.device}")
     return t.data_ptr()
 
 
-def _token_rows(t, name, dtype, T_total, heads, d, dev):
+def _token_rows(t, name, T_total, heads, kv):
     """Address and token stride of [T_total, heads, d] (or [B, T, heads, d]) whose heads and dims
     are contiguous; tokens may lie further apart."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have the cache's dtype {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-    if t.dim() == 4 and t.stride(0) != t.shape[1] * t.stride(1) and t.shape[0] > 1:
+    shape, d = t.shape, kv.d
+    if t.dtype is not kv.dtype:
+        raise TypeError(f"{name} must have the cache's dtype {kv.dtype}, got {t.dtype}")
+    if t.get_device() != kv.index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {kv.device}")
+    if len(shape) not in (3, 4) or shape[-1] != d or (heads is not None and shape[-2] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [.., {heads}, {d}]")
+    if t.numel() != T_total * shape[-2] * d:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {T_total} tokens")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-2] * d
+    stride = t.stride()
+    if len(shape) == 4 and shape[0] > 1 and stride[0] != shape[1] * stride[1]:
         raise ValueError(f"{name}'s tokens must be evenly spaced")
-    if t.dim() not in (3, 4) or t.shape[-1] != d or (heads is not None and t.shape[-2] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [.., {heads}, {d}]")
-    if t.numel() != T_total * t.shape[-2] * d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {T_total} tokens")
-    if (t.stride(-1) != 1 or t.stride(-2) != d) and t.numel() > 0:
+    if stride[-1] != 1 or (stride[-2] != d and shape[-2] > 1):
         raise ValueError(f"{name}'s heads and dims must be contiguous")
-    return t.data_ptr(), t.stride(-3)
+    return t.data_ptr(), stride[-3]
 
 
 def _sequences(x, cu_seqlens, kv):
@@ -630,17 +635,16 @@ def gdn_kv_append(k, v, kv: PagedKV, cu_seqlens=None, pos0=None, *, q=None, q_ou
     (None: no rotation); rope_pos int32 [n_axes, T_total] with rope_sections (a tuple of n_axes
     frequency counts) rotates at other positions than the cache's.  Returns q_out (q's shape,
     contiguous; it may be q itself), or None without q."""
-    dev, dt, d = kv.device, kv.dtype, kv.d
     T_total, N = _sequences(k, cu_seqlens, kv)
-    kp, ks = _token_rows(k, "k", dt, T_total, kv.H_kv, d, dev)
-    vp, vs = _token_rows(v, "v", dt, T_total, kv.H_kv, d, dev)
+    kp, ks = _token_rows(k, "k", T_total, kv.H_kv, kv)
+    vp, vs = _token_rows(v, "v", T_total, kv.H_kv, kv)
     qp, qs, qo, H_q = None, 0, None, 0
     if q is not None:
-        qp, qs = _token_rows(q, "q", dt, T_total, None, d, dev)
+        qp, qs = _token_rows(q, "q", T_total, None, kv)
         H_q = q.shape[-2]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        qo = _addr(q_out, "q_out", dt, q.shape, dev)
+            q_out = torch.empty(q.shape, dtype=kv.dtype, device=kv.device)
+        qo = _addr(q_out, "q_out", kv.dtype, q.shape, kv)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     rope_dims, n_axes, sections = 0, 1, None
@@ -657,10 +661,10 @@ def gdn_kv_append(k, v, kv: PagedKV, cu_seqlens=None, pos0=None, *, q=None, q_ou
         raise ValueError("rope_pos and rope_sections need inv_freq")
     st = lib().gdn_kv_append(
         kv.ref, kp, vp, qp, qo, ks, vs, qs,
-        _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev),
-        _addr(pos0, "pos0", torch.int32, (N,), dev), N, T_total, H_q,
-        _addr(inv_freq, "inv_freq", torch.float32, (rope_dims // 2,), dev), rope_dims,
-        _addr(rope_pos, "rope_pos", torch.int32, (n_axes, T_total), dev), sections, n_axes,
+        _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), kv),
+        _addr(pos0, "pos0", torch.int32, (N,), kv), N, T_total, H_q,
+        _addr(inv_freq, "inv_freq", torch.float32, (rope_dims // 2,), kv), rope_dims,
+        _addr(rope_pos, "rope_pos", torch.int32, (n_axes, T_total), kv), sections, n_axes,
         GDN_ROPE_INTERLEAVED if interleaved else 0, _launch_stream(kv))
     _check(st, "gdn_kv_append")
     return q_out
@@ -686,7 +690,7 @@ def _decode_operands(q, q_pos, kv, out, lse, want_lse, workspace):
     dev = kv.device
     if N > kv.seqs:
         raise ValueError(f"page_table has {kv.seqs} rows for {N} sequences")
-    qp = _addr(q, "q", kv.dtype, q.shape, dev)
+    qp = _addr(q, "q", kv.dtype, q.shape, kv)
     if out is None:
         out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
     if lse is None and want_lse:
@@ -695,9 +699,9 @@ def _decode_operands(q, q_pos, kv, out, lse, want_lse, workspace):
         workspace = attn_decode_workspace(T, H_q, kv.H_kv, kv.d, kv.dtype, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    return (out, lse, N, T, H_q, qp, _addr(q_pos, "q_pos", torch.int32, (N,), dev),
-            _addr(out, "out", kv.dtype, q.shape, dev),
-            _addr(lse, "lse", torch.float32, (N, T, H_q), dev), workspace.data_ptr(),
+    return (out, lse, N, T, H_q, qp, _addr(q_pos, "q_pos", torch.int32, (N,), kv),
+            _addr(out, "out", kv.dtype, q.shape, kv),
+            _addr(lse, "lse", torch.float32, (N, T, H_q), kv), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
 
 
@@ -730,7 +734,7 @@ def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
     L = token_idx.shape[-1]
     shape = (N, L) if T == 1 and token_idx.dim() == 2 else (N, T, L)
     st = lib().gdn_qsa_attn_decode(qp, pp, kv.ref,
-                                   _addr(token_idx, "token_idx", torch.int32, shape, kv.device), L,
+                                   _addr(token_idx, "token_idx", torch.int32, shape, kv), L,
                                    recent, op, lp, N, T, H_q,
                                    kv.d ** -0.5 if scale is None else scale, softcap, wp, wn,
                                    _launch_stream(kv))
@@ -753,7 +757,7 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
     if q.shape[-1] != kv.d:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected head dim {kv.d}")
     dev, H_q = kv.device, q.shape[-2]
-    qp = _addr(q, "q", kv.dtype, q.shape, dev)
+    qp = _addr(q, "q", kv.dtype, q.shape, kv)
     if out is None:
         out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
     if lse is None and want_lse:
@@ -764,11 +768,11 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
             raise ValueError(f"workspace must be contiguous and on {dev}")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = lib().gdn_attn_prefill(
-        qp, kv.ref, _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev),
-        _addr(pos0, "pos0", torch.int32, (N,), dev),
-        _addr(prefix_len, "prefix_len", torch.int32, (N,), dev),
-        _addr(out, "out", kv.dtype, q.shape, dev),
-        _addr(lse, "lse", torch.float32, q.shape[:-1], dev), N, T_total, H_q,
+        qp, kv.ref, _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), kv),
+        _addr(pos0, "pos0", torch.int32, (N,), kv),
+        _addr(prefix_len, "prefix_len", torch.int32, (N,), kv),
+        _addr(out, "out", kv.dtype, q.shape, kv),
+        _addr(lse, "lse", torch.float32, q.shape[:-1], kv), N, T_total, H_q,
         kv.d ** -0.5 if scale is None else scale, softcap, window, wp, wn, _launch_stream(kv))
     _check(st, "gdn_attn_prefill")
     return out, lse

@@ -19,9 +19,10 @@
 //    sums need no exchange.  P goes back to TMEM over the first half of S, as the A operand of PV.
 //    O is rescaled only when a row's maximum grew by more than 2^8 (until then P and l simply use
 //    the old one): after the first tiles that is rare, so no warps are kept for it.
-//  - warp 8: issues the products.  PV(j) and S(j+1) of a tile go out together; S(j+1) overwrites
-//    the columns P(j) was in, after PV(j) read them (one thread's products run in order).
-//  - warp 9 (10 and 11 only fill their warpgroup): loads.  K and V tiles of 128 tokens alternate through a ring, gathered page by page
+//  - warp 8: issues the products.  PV(j) and S(j+1) of a tile go out together;
+//    S(j+1) overwrites the columns P(j) was in, after PV(j) read them (one thread's products run
+//    in order).
+//  - warp 10 (9 and 11 only fill the warpgroup): loads.  K and V tiles of 128 tokens alternate through a ring, gathered page by page
 //    with TMA; tokens that are absent are left out of the softmax by a mask, and their V rows (and
 //    those past the sequence) are zeroed, so nothing a dead row holds reaches a product.
 #include <cuda.h>
@@ -48,9 +49,57 @@ constexpr int kTile = 128;                 // query rows of a tile, tokens of a 
 constexpr uint32_t kPollNs = 2000, kDrainBudget = GDN_DEFAULT_WAIT_BUDGET;
 constexpr float kLazy = 8.f;               // growth of a row maximum (base 2) that O may lag
 
+// Two fp32 lanes per instruction, and the larger of three.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// cap2 tanh(y) + add for |y| <= 1: tanh(y) = y R(y^2), R of degree 5 fitted to the least largest
+// relative error over [0, 1] (5.9e-7).
+__device__ __forceinline__ float2 capped_near2(float2 y, float cap2, float2 add) {
+    const float c[6] = {0.9999994136f * cap2, -0.3332904242f * cap2, 0.1328143402f * cap2,
+                        -0.0516056755f * cap2, 0.0167431149f * cap2, -0.0030670597f * cap2};
+    const float2 t = mul2(y, y);
+    float2 r = make_float2(c[5], c[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) r = fma2(r, t, make_float2(c[i], c[i]));
+    return fma2(y, r, add);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 enum Bar {
     B_Q = 0, B_FULL = 1, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2,
-    B_O = B_P + 2, B_FIX = B_O + 2, B_DRAIN, B_COUNT
+    B_O = B_P + 4, B_FIX = B_O + 2, B_DRAIN, B_COUNT                    // B_P: tile x part
 };
 
 template <int D>
@@ -75,7 +124,8 @@ template <int N> __device__ __forceinline__ void regs_give() {
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uint32_t budget,
                                           const volatile int *abort_flag) {
     for (uint32_t i = 0; i < budget; ++i) {
-        if (mbar_try_wait_sleep(bar, parity, kPollNs)) return true;
+        // (the timed form costs a few hundred cycles even when the phase is over)
+        if (i < 64 ? mbar_try_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kPollNs)) return true;
         if (*abort_flag) return false;
     }
     return false;
@@ -93,11 +143,17 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bt_tile = kTile >> p.pack_shift, bt = 2 * bt_tile;        // tokens of a tile, block
     int n, blk;
-    if (!find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; }, blockIdx.x, n, blk))
+    const int packs = p.G >> p.pack_shift, heads = p.cache.H_kv * packs;
+    // Heads take turns when one head's blocks do not fill the SMs (so the longest blocks of all of
+    // them start first: 442 against 474 us on 137 blocks x 4 heads), and follow one another when
+    // they do (then all SMs read the same K and V: 126 against 130 us on 256 blocks x 2 heads).
+    const int blocks = gridDim.x / heads;
+    const int hx = p.heads_first ? blockIdx.x % heads : blockIdx.x / blocks;
+    if (!find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; },
+                              p.heads_first ? blockIdx.x / heads : blockIdx.x % blocks, n, blk))
         return;
-    const int packs = p.G >> p.pack_shift;
-    const int hk = blockIdx.y / packs;                                   // key head
-    const int h0 = hk * p.G + (blockIdx.y % packs << p.pack_shift);      // first query head
+    const int hk = hx / packs;                                           // key head
+    const int h0 = hk * p.G + (hx % packs << p.pack_shift);              // first query head
     const Tokens seq = sequence_of(p, n);
     const long long first = seq.first;
     const int len = seq.len;
@@ -105,22 +161,19 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int e = see.e;
     const int q0 = blk * bt;
     const int k_lo = see.lo(q0), k_base = k_lo / kTile * kTile;          // oldest token seen, its tile
-    int tiles[2];                                                        // K / V tiles each row tile walks
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    auto tiles_of = [&](int i) -> int {                                  // K / V tiles row tile i walks
         const int a = q0 + i * bt_tile;
-        const int last = min(a + bt_tile, len) - 1;
-        const int hi = a < len ? see.hi(last) : 0;
-        tiles[i] = hi > k_base ? (hi - k_base + kTile - 1) / kTile : 0;
-    }
-    const int nt = max(tiles[0], tiles[1]);
+        const int hi = a < len ? see.hi(min(a + bt_tile, len) - 1) : 0;
+        return hi > k_base ? (hi - k_base + kTile - 1) / kTile : 0;
+    };
+    const int tiles_a = tiles_of(0), tiles_b = tiles_of(1), nt = max(tiles_a, tiles_b);
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
     if (warp == 8) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
     if (tid == 0) {
-        for (int b = 0; b < B_COUNT; ++b) mbar_init(bars + b, b == B_P || b == B_P + 1 ? 128 : 1);
+        for (int b = 0; b < B_COUNT; ++b) mbar_init(bars + b, b >= B_P && b < B_P + 4 ? 4 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -141,7 +194,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp < 8) {
         // ==================================================================== softmax
         regs_take<kRegsSoftmax>();
-        const int i = warp >> 2, row = tid & 127;
+        const int i = warp >> 2, row = tid & 127, tiles = i ? tiles_b : tiles_a;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + kTmS + 128 * i, o_at = tmem + lanes + kTmO + 128 * i;
         const int tok = q0 + i * bt_tile + (row >> p.pack_shift);
@@ -151,10 +204,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int lo_max = see.lo(q0 + (i + 1) * bt_tile - 1), hi_min = see.hi(q0 + i * bt_tile);
         float m = -INFINITY, l = 0.f;                                    // m in base-2 units
         bool ok = true;
-        const float k2 = CAP ? p.scale * (2.f * kLog2e / p.cap) : p.scale2;
-        const float cap2 = p.cap * kLog2e;
+        const float k2 = CAP ? fabsf(p.scale) * (2.f * kLog2e / p.cap) : p.scale2;
+        const float cap2 = p.cap * kLog2e, ky = CAP ? fabsf(p.scale) / p.cap : 0.f;
 #pragma unroll 1
-        for (int j = 0; j < tiles[i]; ++j) {
+        for (int j = 0; j < tiles; ++j) {
             if (!__all_sync(0xffffffffu, wait(B_S + i, j))) { fail(1 + i); ok = false; break; }
             tc_fence_after();
             uint32_t raw[4][32];
@@ -165,12 +218,24 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tmem_wait_ld();
             float s[128];
 #pragma unroll
-            for (int c = 0; c < 128; ++c) {
-                const float x = __uint_as_float(raw[c >> 5][c & 31]);
-                s[c] = CAP ? capped2(x, k2, cap2) : x;
-            }
+            for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
             const bool whole = k0 >= lo_max && k0 + kTile <= hi_min &&
                                (pm.x & pm.y & pm.z & pm.w) == 0xffffffffu;
+            // tanh(y) = y R(y^2) on the FMA pipe while no score of the warp's rows passes the cap
+            // (|y| <= 1), else by exponentials (two more per score on the busiest pipe)
+            bool near = false;
+            if (CAP) {
+                if (whole) {
+                    float far = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
+                    near = __all_sync(0xffffffffu, far * ky <= 1.f);
+                }
+                if (!near) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = capped2(s[c], k2, cap2);
+                }
+            }
             if (!whole) {
                 const uint32_t pw[4] = {pm.x, pm.y, pm.z, pm.w};
                 const int a = lo - k0, z = hi - k0;
@@ -188,9 +253,12 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < 128; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            if (!CAP && mx != -INFINITY) mx *= k2;
+            for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
+            float mx = max3(fmaxf(mx4[0], s[124]), fmaxf(mx4[1], s[125]),
+                            fmaxf(fmaxf(mx4[2], s[126]), fmaxf(mx4[3], s[127])));
+            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped2(mx, k2, cap2) : mx * k2;
             const bool grow = mx > m + kLazy;                            // also when m is -inf
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2(m - mx) : 1.f;                // 0 from -inf
@@ -210,29 +278,44 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             const float shift = m == -INFINITY ? 0.f : m;
-            // each weight is rounded to bf16 for the product (off by 2^-8 of itself at most);
-            // the sum takes the unrounded ones
-            float sum[2] = {0.f, 0.f};
+            // Each weight is rounded to bf16 for the product (off by 2^-8 of itself at most); the
+            // sum takes the unrounded ones.  P goes out in two parts: PV of the first 96 tokens
+            // runs while the last 32 weights are formed.
+            const float2 kk = make_float2(CAP ? 1.f : k2, CAP ? 1.f : k2), sh = make_float2(-shift, -shift);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto publish = [&](int part) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(bars + B_P + 2 * i + part);
+            };
+            auto all_weights = [&](auto &&exponent) {
+                auto weights = [&](int at) -> uint32_t {
+                    const float2 x = exponent(make_float2(s[at], s[at + 1]));
+                    const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                    sum[at >> 1 & 1] = add2(sum[at >> 1 & 1], w);
+                    return pack2(w.x, w.y);
+                };
+                uint32_t w32[32], w16[16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[32];
+                for (int x = 0; x < 32; ++x) w32[x] = weights(2 * x);
+                tmem_st32(s_at, w32);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const int at = 64 * c + 2 * x;
-                    const float a = CAP ? ex2(s[at] - shift) : ex2(fmaf(s[at], k2, -shift));
-                    const float b = CAP ? ex2(s[at + 1] - shift) : ex2(fmaf(s[at + 1], k2, -shift));
-                    sum[0] += a;
-                    sum[1] += b;
-                    w[x] = pack2(a, b);
-                }
-                tmem_st32(s_at + 32 * c, w);
-            }
-            l += sum[0] + sum[1];
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive_local(bars + B_P + i);
+                for (int x = 0; x < 16; ++x) w16[x] = weights(64 + 2 * x);
+                tmem_st16(s_at + 32, w16);
+                publish(0);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) w16[x] = weights(96 + 2 * x);
+                tmem_st16(s_at + 48, w16);
+            };
+            if (CAP && near)
+                all_weights([&](float2 x) { return capped_near2(mul2(x, make_float2(ky, ky)), cap2, sh); });
+            else
+                all_weights([&](float2 x) { return fma2(x, kk, sh); });
+            l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
+            publish(1);
         }
-        if (ok && tiles[i] > 0 && !__all_sync(0xffffffffu, wait(B_O + i, 0))) {
+        if (ok && tiles > 0 && !__all_sync(0xffffffffu, wait(B_O + i, 0))) {
             fail(3 + i);
             ok = false;
         }
@@ -245,7 +328,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                if (tiles[i] > 0) {
+                if (tiles > 0) {
                     tmem_ld32(o_at + 32 * c, o);
                     tmem_wait_ld();
                 } else {
@@ -269,66 +352,79 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     } else {
         regs_give<kRegsOther>();
         if (warp == 8) {
-        // =================================================================== products
-        if (lane == 0 && nt > 0) {
-            const uint32_t neg = p.scale < 0.f && !CAP ? 1u << 14 : 0u;  // scale2 is |scale|
+            // =============================================================== products
+            // Tile A's and tile B's turns alternate, which keeps the two softmax warpgroups half a period
+            // apart (one issuing warp for each lets them fall into step).  The whole warp walks this code and one elected lane issues: descriptors then
+            // stay in uniform registers (issued from a divergent thread, a product took 60-100 cycles).
+            const uint32_t neg = p.scale < 0.f ? 1u << 14 : 0u;          // the softmax takes |scale|
             const uint32_t id_s = idesc_bf16(128, 128, false, false) | neg;
             const uint32_t id_o = idesc_bf16(128, D, false, true);
-            const uint32_t ring = smem_u32(sm + L::kRing), qs = smem_u32(sm + L::kQ);
-            auto scores = [&](int i, int j) {
-                const uint32_t kt = ring + (2 * j % kSlots) * L::kTileBytes;
-                const uint32_t qt = qs + i * L::kTileBytes;
+            const uint64_t q_desc = sdesc_kmajor(smem_u32(sm + L::kQ));
+            const uint64_t k_desc = sdesc_kmajor(smem_u32(sm + L::kRing));
+            const uint64_t v_desc = sdesc_mnmajor(smem_u32(sm + L::kRing), L::kHalf);
+            const bool leader = elect_one();
+            auto scores = [&](int i, int slot) {
+                const uint64_t a = q_desc + i * (L::kTileBytes >> 4), b = k_desc + slot * (L::kTileBytes >> 4);
+                if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
-                    umma_bf16(tmem + kTmS + 128 * i, sdesc_kmajor(qt + off), sdesc_kmajor(kt + off), id_s, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+                        umma_bf16(tmem + kTmS + 128 * i, a + off, b + off, id_s, ks > 0);
+                    }
                 }
             };
-            bool ok = wait(B_Q, 0) && wait(B_FULL, 0);
+            auto commit = [&](int b) { if (leader) umma_commit(bars + b); };
+            auto ready = [&](int b, int k) -> bool { return __all_sync(0xffffffffu, wait(b, k)); };
+            bool ok = true;
             int issued = 0;
-            if (ok) {
+            if (nt > 0 && (ok = ready(B_Q, 0) && ready(B_FULL, 0))) {
                 tc_fence_after();
-                for (int i = 0; i < 2; ++i)
-                    if (tiles[i] > 0) { scores(i, 0); umma_commit(bars + B_S + i); issued = 1; }
-                umma_commit(bars + B_EMPTY + 0);
+                issued = 1;
+                if (tiles_a > 0) { scores(0, 0); commit(B_S); }
+                if (tiles_b > 0) { scores(1, 0); commit(B_S + 1); }
+                commit(B_EMPTY);
             }
 #pragma unroll 1
             for (int j = 0; ok && j < nt; ++j) {
-                const int vs = (2 * j + 1) % kSlots;
-                ok = wait(B_FULL + vs, (2 * j + 1) / kSlots);
-                if (ok && j + 1 < nt) ok = wait(B_FULL + (2 * j + 2) % kSlots, (2 * j + 2) / kSlots);
-                if (!ok) break;
-#pragma unroll 1
-                for (int i = 0; ok && i < 2; ++i) {
-                    if (j >= tiles[i]) continue;
-                    if (!(ok = wait(B_P + i, j))) break;
-                    tc_fence_after();
-                    const uint32_t vt = ring + vs * L::kTileBytes;
+                const int vs = (2 * j + 1) % kSlots, ks = (2 * j + 2) % kSlots;
+                const uint64_t b = v_desc + vs * (L::kTileBytes >> 4);
+                ok = ready(B_FULL + vs, (2 * j + 1) / kSlots);
+                if (ok && j + 1 < nt) ok = ready(B_FULL + ks, (2 * j + 2) / kSlots);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        umma_bf16_ta(tmem + kTmO + 128 * i, tmem + kTmS + 128 * i + 8 * ks,
-                                     sdesc_mnmajor(vt + ks * 2048, L::kHalf), id_o, j > 0 || ks > 0);
-                    if (j + 1 < tiles[i]) {
-                        scores(i, j + 1);
-                        umma_commit(bars + B_S + i);
-                    } else {
-                        umma_commit(bars + B_O + i);
+                for (int i = 0; i < 2; ++i) {
+                    const int tiles = i ? tiles_b : tiles_a;
+                    const uint32_t s_at = tmem + kTmS + 128 * i, o_at = tmem + kTmO + 128 * i;
+                    if (!ok || j >= tiles) continue;
+                    if (!(ok = ready(B_P + 2 * i, j))) continue;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < 6; ++k)
+                            umma_bf16_ta(o_at, s_at + 8 * k, b + k * (2048 >> 4), id_o, j > 0 || k > 0);
                     }
+                    if (!(ok = ready(B_P + 2 * i + 1, j))) continue;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 6; k < 8; ++k)
+                            umma_bf16_ta(o_at, s_at + 8 * k, b + k * (2048 >> 4), id_o, 1);
+                    }
+                    if (j + 1 < tiles) scores(i, ks);
+                    commit((j + 1 < tiles ? B_S : B_O) + i);
                 }
                 if (!ok) break;
-                umma_commit(bars + B_EMPTY + vs);
-                if (j + 1 < nt) umma_commit(bars + B_EMPTY + (2 * j + 2) % kSlots);
+                commit(B_EMPTY + vs);
+                if (j + 1 < nt) commit(B_EMPTY + ks);
             }
             if (!ok) {
-                fail(5);
+                if (lane == 0) fail(5);
                 if (issued) {                                            // let the products end first
-                    umma_commit(bars + B_DRAIN);
+                    commit(B_DRAIN);
                     mbar_wait(bars + B_DRAIN, 0, kDrainBudget);
                 }
             }
-        }
-        __syncwarp();
-        } else if (warp == 9) {
+            __syncwarp();
+        } else if (warp == 10) {
         // ====================================================================== loads
         const int ps = 1 << p.cache.page_shift, box = ps < kTile ? ps : kTile;
         const int boxes = kTile / box;
@@ -442,12 +538,13 @@ bool make_map(CUtensorMap *map, const void *base, long long rows, int heads, int
 template <int D, bool CAP> PerDevice g_setup;
 
 template <int D, bool CAP>
-cudaError_t launch_tc(const AttnPrefillParams &p, const gdn_paged_kv &kv, cudaStream_t stream) {
+cudaError_t launch_tc(AttnPrefillParams p, const gdn_paged_kv &kv, cudaStream_t stream) {
     constexpr int smem = Smem<D>::kTotal;
+    int sms = 0;
     cudaError_t e = g_setup<D, CAP>.ensure([] {
         return cudaFuncSetAttribute(attn_prefill_kernel<D, CAP>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    });
+    }, &sms);
     if (e != cudaSuccess) return e;
     const int pack = 1 << p.pack_shift, bt = 2 * (kTile >> p.pack_shift);
     const int box = kv.page_size < kTile ? kv.page_size : kTile;
@@ -459,8 +556,10 @@ cudaError_t launch_tc(const AttnPrefillParams &p, const gdn_paged_kv &kv, cudaSt
         return cudaErrorInvalidValue;
     // at most one block per sequence is not full
     const long long blocks = p.cu ? p.T_total / bt + p.N : (p.T_seq + bt - 1) / bt * p.N;
-    attn_prefill_kernel<D, CAP><<<dim3((unsigned)blocks, (unsigned)(kv.H_kv * (p.G >> p.pack_shift))),
-                                  kThreads, smem, stream>>>(mq, mk, mv, p);
+    const long long grid = blocks * kv.H_kv * (p.G >> p.pack_shift);
+    p.heads_first = blocks < sms;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    attn_prefill_kernel<D, CAP><<<(unsigned)grid, kThreads, smem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 

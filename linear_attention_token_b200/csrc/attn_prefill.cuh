@@ -16,6 +16,7 @@ struct AttnPrefillParams {
     const int32_t *cu, *pos0, *prefix;
     long long T_total, T_seq;              // T_seq: tokens per sequence when cu is null
     int N, H_q, G, window;
+    bool heads_first;                      // order of the CTAs
     int pack_shift;                        // rows of a tile: token r >> pack_shift, head the rest
     float scale2, cap;                     // |scale| log2 e; 0: no cap
     float scale;
