@@ -678,7 +678,8 @@ def gdn_attn_decode_workspace_size(n_queries: int, H_q: int, H_kv: int, d: int,
 
 def attn_decode_workspace(n_queries: int, H_q: int, H_kv: int, d: int, dtype=torch.bfloat16,
                           device="cuda") -> torch.Tensor:
-    """A workspace for gdn_attn_decode and gdn_qsa_attn_decode (any contents)."""
+    """A workspace for gdn_attn_decode and gdn_qsa_attn_decode (any contents).  Calls that may
+    overlap on the GPU need one each."""
     n = gdn_attn_decode_workspace_size(n_queries, H_q, H_kv, d, dtype)
     return torch.empty(n, dtype=torch.uint8, device=device)
 

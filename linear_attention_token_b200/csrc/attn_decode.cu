@@ -15,7 +15,9 @@
 //    stretch of it, wherever units begin and end: ragged lengths cost nothing, one long
 //    sequence uses every SM, and no length is needed on the host (a captured graph stays valid
 //    as sequences grow).  A unit that lies in one CTA is finished there; the parts of the
-//    others go to the workspace (at most two per CTA) and attn_join_kernel joins them.
+//    others go to the workspace (at most two per CTA), and attn_join_kernel, launched beside this
+//    one, joins them.  (The last CTA of a unit joining in this kernel was slower on every size: one
+//    CTA's fences, atomics and cold code at the end cost more than a second grid.)
 //  - bf16: a warp owns 16 query rows as one mma.sync m16n8k16 row tile.  With few rows the
 //    product is far from the tensor pipe's limit, so what counts is that loads never pause:
 //    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
@@ -24,6 +26,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "attn_math.cuh"
 #include "device_once.h"
 #include "paged_kv.cuh"
 
@@ -35,7 +38,6 @@ constexpr int kStep = 64;                  // keys per step of a CTA, 16 per war
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kLoadRows = 16;              // keys one warp loads per step
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What CTA c leaves for the join: the unit that began in it and ends in a later CTA.
 struct JoinRecord {
@@ -57,7 +59,7 @@ struct DecodeParams {
     int rows, row_blocks;                  // query rows of a unit (before blocking), blocks
     int units_per_seq;
     int list_len, recent, window;
-    float scale, cap;                      // score multiplier; 0: no cap
+    Scoring score;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -72,19 +74,6 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Scores in the base-2 domain: log2(e) times the scaled, capped score.  tanh(y) is written
-// 1 - 2 / (1 + e^{2y}): its absolute error stays at a few 2^-24 of the cap.
-__device__ __forceinline__ float score2(float dot, float scale, float cap) {
-    if (cap == 0.f) return dot * (scale * kLog2e);
-    const float e = ex2(dot * scale * (2.f * kLog2e / cap));
-    return cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
-}
-
 // --------------------------------------------------------------------- where the work is
 // Keys that unit (n, sub) walks: dense, tokens [lo, hi) with lo on a step; lists, positions
 // of list (padded to a step) and newest tokens.
@@ -133,40 +122,38 @@ __device__ __forceinline__ size_t row_head(const DecodeParams &p, const Unit &u,
 }
 
 // ------------------------------------------------------------------------------- loading
-// One warp's 16 keys of one step into its 16 rows of a stage (rows of D elements, 16-byte
-// chunk c of row r at c ^ (r & 7)), keys at kdst, values at vdst; returns the mask of keys that
-// are present.  Absent keys are zero-filled, so nothing a dead row holds reaches a product.
-template <typename E, int D, bool LIST>
-__device__ __forceinline__ uint32_t load_keys(const DecodeParams &p, const Unit &u, const Span &sp,
-                                              long long pos, int step, int sub, uint32_t kdst,
-                                              uint32_t vdst) {
-    constexpr int CH = D * (int)sizeof(E) / 16, RPI = 32 / CH, ITER = kLoadRows / RPI;
-    const int lane = threadIdx.x & 31, key = lane & 15;
-    int row;                               // cache row of key `key`
+// Token of key `key` (0..15) of warp `sub`'s share of a step, or -1: not seen by any query of the
+// unit.  (What nobody sees is not read: it may hold anything.)
+template <bool LIST>
+__device__ __forceinline__ int token_at(const DecodeParams &p, const Unit &u, const Span &sp,
+                                        long long pos, int step, int sub, int key) {
+    const int i = step * kStep + sub * kLoadRows + key;
     if (LIST) {
-        const int i = step * kStep + sub * kLoadRows + key;
         const int list_pad = (p.list_len + kStep - 1) / kStep * kStep;
         const long long at = pos + u.j;
-        long long t = -1;
         if (i < list_pad) {
-            if (i < p.list_len) {
-                t = __ldg(p.list + ((size_t)u.n * p.T + u.j) * p.list_len + i);
-                if (t > at - p.recent) t = -1;
-            }
-        } else if (i - list_pad < p.recent) {
-            t = at - p.recent + 1 + (i - list_pad);
+            if (i >= p.list_len) return -1;
+            const int t = __ldg(p.list + ((size_t)u.n * p.T + u.j) * p.list_len + i);
+            return t <= at - p.recent ? t : -1;
         }
-        row = cache_row(p.cache, u.n, t);
-    } else {
-        const long long t = sp.lo + (long long)step * kStep + sub * kLoadRows + key;
-        // what no query sees is not read: it may hold anything
-        const bool seen = t < pos + p.T && (p.window <= 0 || t > pos - p.window);
-        row = seen ? cache_row(p.cache, u.n, t) : -1;
+        const long long t = at - p.recent + 1 + (i - list_pad);
+        return i - list_pad < p.recent && t >= 0 && t <= INT32_MAX ? (int)t : -1;
     }
-    const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-    const int c = lane % CH;
+    const long long t = sp.lo + i;
+    const bool seen = t < pos + p.T && (p.window <= 0 || t > pos - p.window) && t <= INT32_MAX;
+    return seen ? (int)t : -1;
+}
+
+// One warp's 16 keys of one step into its 16 rows of a stage (rows of D elements, 16-byte
+// chunk c of row r at c ^ (r & 7)), keys at kdst, values at vdst.  Lane l < 16 holds the cache row
+// of key l; absent keys (-1) are zero-filled, so nothing a dead row holds reaches a product.
+template <typename E, int D>
+__device__ __forceinline__ void load_keys(const DecodeParams &p, int h, int row, uint32_t kdst,
+                                          uint32_t vdst) {
+    constexpr int CH = D * (int)sizeof(E) / 16, RPI = 32 / CH, ITER = kLoadRows / RPI;
+    const int lane = threadIdx.x & 31, c = lane % CH;
     const size_t pitch = (size_t)p.cache.H_kv * D * sizeof(E);
-    const size_t off = (size_t)u.h * D * sizeof(E) + (size_t)c * 16;
+    const size_t off = (size_t)h * D * sizeof(E) + (size_t)c * 16;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int r = lane / CH + i * RPI;
@@ -176,7 +163,6 @@ __device__ __forceinline__ uint32_t load_keys(const DecodeParams &p, const Unit 
         cp_async16(kdst + d, p.cache.k + src, at >= 0);
         cp_async16(vdst + d, p.cache.v + src, at >= 0);
     }
-    return present;
 }
 
 // ------------------------------------------------------------------- bf16: tensor cores
@@ -195,11 +181,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // A warp's 16 query rows against the keys of its team.  Lane (g = lane / 4, c = lane % 4) holds
 // rows g and g + 8: scores of keys 8 i + 2 c, + 1; outputs of dims 8 i + 2 c, + 1.
 template <int D, int TEAM, bool LIST>
@@ -256,6 +237,7 @@ struct TensorRows {
                 mma16816(s[2 * i + 1], q[k], b[2], b[3]);
             }
         }
+        score2(reinterpret_cast<float(&)[NT * 4]>(s), p.score);
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -267,7 +249,7 @@ struct TensorRows {
                     const int t = (int)(token0 + key);
                     live = live && t <= last[e >> 1] && t >= first[e >> 1];
                 }
-                s[i][e] = live ? score2(s[i][e], p.scale, p.cap) : -INFINITY;
+                s[i][e] = live ? s[i][e] : -INFINITY;
                 mx[e >> 1] = fmaxf(mx[e >> 1], s[i][e]);
             }
         float shift[2];
@@ -382,14 +364,16 @@ struct FmaRows {
         float *w = shared + R * D + (threadIdx.x >> 5) * R * 16;
         const long long t = token0 + key;
 #pragma unroll
+        for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+        score2(s, p.score);
+#pragma unroll
         for (int r = 0; r < R; ++r) {
-            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
             bool live = (present >> key) & 1;
             if (!LIST) {
                 const long long at = pos0 + (row0 + r) / p.G;
                 live = live && t <= at && (p.window <= 0 || t > at - p.window);
             }
-            const float x = live ? score2(s[r], p.scale, p.cap) : -INFINITY;
+            const float x = live ? s[r] : -INFINITY;
             float mx = x;
 #pragma unroll
             for (int d = 2; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -450,14 +434,6 @@ struct Layout {
     static constexpr int kSmem = kBody + kExtra + kMask + 64;
 };
 
-template <typename E> __device__ __forceinline__ void store2(void *p, size_t i, float a, float b);
-template <> __device__ __forceinline__ void store2<float>(void *p, size_t i, float a, float b) {
-    *reinterpret_cast<float2 *>(static_cast<float *>(p) + i) = make_float2(a, b);
-}
-template <> __device__ __forceinline__ void store2<__nv_bfloat16>(void *p, size_t i, float a, float b) {
-    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + i) = pack2(a, b);
-}
-
 template <int TEAM> __device__ __forceinline__ void team_sync() {
     if (TEAM == 1) __syncwarp();
     else if (TEAM == kWarps) __syncthreads();
@@ -465,9 +441,64 @@ template <int TEAM> __device__ __forceinline__ void team_sync() {
 }
 
 // First step of CTA c's stretch when G CTAs share W steps, and the CTA that runs step x.
-__device__ __forceinline__ long long stretch(long long W, int G, int c) { return W * c / G; }
+__device__ __forceinline__ long long stretch(long long W, int G, int c) {
+    const unsigned long long x = (unsigned long long)W * c;
+    return x >> 32 ? (long long)(x / G) : (long long)((uint32_t)x / (uint32_t)G);
+}
 __device__ __forceinline__ int cta_of(long long W, int G, long long x) {
-    return (int)(((x + 1) * G + W - 1) / W) - 1;
+    const unsigned long long y = (unsigned long long)(x + 1) * G + W - 1;
+    return (y >> 32 ? (int)(y / W) : (int)((uint32_t)y / (uint32_t)W)) - 1;
+}
+
+// Four output columns of one row: maximum m, sum l, columns o.
+struct Sums {
+    float m, l;
+    float4 o;
+};
+// The sums of up to N parts: their m and l, and their columns, are loaded together, and the weights
+// e^{m_i - m} do not depend on one another.
+template <int N, class ML, class O>
+__device__ __forceinline__ Sums sum_parts(int count, ML &&ml_of, O &&o_of) {
+    float2 ml[N];
+    float4 o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        ml[i] = i < count ? ml_of(i) : make_float2(-INFINITY, 0.f);
+        o[i] = i < count ? o_of(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    Sums s;
+    s.m = ml[0].x;
+#pragma unroll
+    for (int i = 1; i < N; ++i) s.m = fmaxf(s.m, ml[i].x);
+    const float shift = s.m == -INFINITY ? 0.f : s.m;
+    s.l = 0.f;
+    s.o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float f = ex2(ml[i].x - shift);
+        s.l = fmaf(ml[i].y, f, s.l);
+        s.o.x = fmaf(o[i].x, f, s.o.x);
+        s.o.y = fmaf(o[i].y, f, s.o.y);
+        s.o.z = fmaf(o[i].z, f, s.o.z);
+        s.o.w = fmaf(o[i].w, f, s.o.w);
+    }
+    return s;
+}
+
+template <typename E> __device__ __forceinline__ void store4(void *p, size_t i, float4 x);
+template <> __device__ __forceinline__ void store4<float>(void *p, size_t i, float4 x) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = x;
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(void *p, size_t i, float4 x) {
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
+}
+
+template <typename E, int D, bool LIST>
+__device__ __forceinline__ void finish(const DecodeParams &p, const Unit &u, int row, int c, const Sums &s) {
+    const size_t rh = row_head<LIST>(p, u, row);
+    const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
+    store4<E>(p.out, rh * D + c, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
+    if (c == 0 && p.lse) p.lse[rh] = s.l > 0.f ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
 }
 
 template <class ROWS, int D, bool LIST>
@@ -477,45 +508,65 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using L = Layout<ROWS, D>;
     constexpr int TEAM = ROWS::kTeam;
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ long long scan[kThreads];
-    __shared__ long long found[2];
+    __shared__ long long sums[kWarps], found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *extra = reinterpret_cast<float *>(sm + L::kBody);
     uint32_t *masks = reinterpret_cast<uint32_t *>(sm + L::kBody + L::kExtra);   // [stage][warp]
 
     pdl_trigger();
-    // all steps, and where this CTA's stretch begins: thread t sums sequences [t per, t per + per)
-    const int per = (p.N + kThreads - 1) / kThreads;
-    const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
-    long long mine = 0;
-    for (int n = n0; n < n1; ++n) mine += (long long)span_of<LIST>(p, n).steps * p.units_per_seq;
-    scan[tid] = mine;
-    __syncthreads();
-    for (int d = 1; d < kThreads; d <<= 1) {
-        const long long x = tid >= d ? scan[tid - d] : 0;
-        __syncthreads();
-        scan[tid] += x;
-        __syncthreads();
-    }
-    const long long W = scan[kThreads - 1];
-    const int G = (int)(W < (long long)gridDim.x ? W : gridDim.x);
+    // all steps, and where this CTA's stretch begins
     const int cta = blockIdx.x;
     if (tid == 0) p.rec[cta].parts = 0;
-    if (cta >= G) return;
-    const long long begin = stretch(W, G, cta), end = stretch(W, G, cta + 1);
-    const long long before = scan[tid] - mine;
-    if (before <= begin && begin < scan[tid]) {
-        long long at = before;
-        for (int n = n0; n < n1; ++n) {
-            const long long x = (long long)span_of<LIST>(p, n).steps * p.units_per_seq;
-            if (begin < at + x) { found[0] = n; found[1] = begin - at; break; }
-            at += x;
+    long long W, begin, end;
+    int G, n, sub, step;
+    Span sp;
+    if (LIST) {                            // every unit has the same steps
+        sp = span_of<LIST>(p, 0);
+        W = (long long)p.N * p.units_per_seq * sp.steps;
+        G = (int)(W < (long long)gridDim.x ? W : gridDim.x);
+        if (cta >= G) return;
+        begin = stretch(W, G, cta);
+        const long long unit = begin / sp.steps;
+        step = (int)(begin - unit * sp.steps);
+        n = (int)(unit / p.units_per_seq);
+        sub = (int)(unit - (long long)n * p.units_per_seq);
+    } else {                               // thread t sums sequences [t per, t per + per)
+        const int per = (p.N + kThreads - 1) / kThreads;
+        const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+        long long mine = 0;
+        for (int i = n0; i < n1; ++i) mine += (long long)span_of<LIST>(p, i).steps * p.units_per_seq;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
         }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        W = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += sums[w];
+            W += sums[w];
+        }
+        G = (int)(W < (long long)gridDim.x ? W : gridDim.x);
+        if (cta >= G) return;
+        begin = stretch(W, G, cta);
+        if (upto - mine <= begin && begin < upto) {
+            long long at = upto - mine;
+            for (int i = n0; i < n1; ++i) {
+                const long long x = (long long)span_of<LIST>(p, i).steps * p.units_per_seq;
+                if (begin < at + x) { found[0] = i; found[1] = begin - at; break; }
+                at += x;
+            }
+        }
+        __syncthreads();
+        n = (int)found[0];
+        sp = span_of<LIST>(p, n);
+        sub = (int)(found[1] / sp.steps);
+        step = (int)(found[1] - (long long)sub * sp.steps);
     }
-    __syncthreads();
-    int n = (int)found[0];
-    Span sp = span_of<LIST>(p, n);
-    int sub = (int)(found[1] / sp.steps), step = (int)(found[1] % sp.steps);
+    end = stretch(W, G, cta + 1);
 
     ROWS rows;
     const int team = warp / TEAM;
@@ -524,15 +575,24 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         const Unit u = unit_of<LIST>(p, n, sub);
         const long long pos = __ldg(p.q_pos + n);
         const int count = (int)min((long long)(sp.steps - step), end - at);
+        // tokens are looked up two steps, cache rows one step before their loads go out, so that
+        // the chain list -> page table -> key never stalls a step
+        auto token = [&](int i) {
+            return i < count ? token_at<LIST>(p, u, sp, pos, step + i, warp, lane & 15) : -1;
+        };
+        int row = cache_row(p.cache, n, token(0)), t_ahead = token(1);
         auto load = [&](int i) {
+            const int row_ahead = cache_row(p.cache, n, t_ahead);
+            t_ahead = token(i + 2);
             if (i < count) {
                 const int st = i % kStages;
                 const uint32_t dst = ring + st * 2 * L::kStageBytes + warp * kLoadRows * L::kRowBytes;
-                const uint32_t m = load_keys<E, D, LIST>(p, u, sp, pos, step + i, warp, dst,
-                                                         dst + L::kStageBytes);
-                if (lane == 0) masks[st * kWarps + warp] = m;
+                load_keys<E, D>(p, u.h, row, dst, dst + L::kStageBytes);
+                const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+                if (lane == 0) masks[st * kWarps + warp] = present;
             }
             cp_commit();
+            row = row_ahead;
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i);
@@ -559,31 +619,17 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         const bool whole = count == sp.steps;
         const int slot = at == begin ? 0 : 1;
         const int live_rows = min(ROWS::kRows, p.rows - u.rb * ROWS::kRows);
-        for (int i = tid; i < live_rows * (D / 2); i += kThreads) {
-            const int r = i / (D / 2), c = 2 * (i % (D / 2));
-            float m = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < L::kTeams; ++t) m = fmaxf(m, sml[t * ROWS::kRows + r].x);
-            const float shift = m == -INFINITY ? 0.f : m;
-            float l = 0.f, a = 0.f, b = 0.f;
-#pragma unroll
-            for (int t = 0; t < L::kTeams; ++t) {
-                const float2 ml = sml[t * ROWS::kRows + r];
-                const float f = ex2(ml.x - shift);
-                const float2 x = *reinterpret_cast<const float2 *>(so + (t * ROWS::kRows + r) * D + c);
-                l = fmaf(ml.y, f, l);
-                a = fmaf(x.x, f, a);
-                b = fmaf(x.y, f, b);
-            }
+        for (int i = tid; i < live_rows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = 4 * (i % (D / 4));
+            const Sums s = sum_parts<L::kTeams>(
+                L::kTeams, [&](int t) { return sml[t * ROWS::kRows + r]; },
+                [&](int t) { return *reinterpret_cast<const float4 *>(so + (t * ROWS::kRows + r) * D + c); });
             if (whole) {
-                const size_t rh = row_head<LIST>(p, u, u.rb * ROWS::kRows + r);
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                store2<E>(p.out, rh * D + c, a * inv, b * inv);
-                if (c == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                finish<E, D, LIST>(p, u, u.rb * ROWS::kRows + r, c, s);
             } else {
                 const size_t pr = ((size_t)cta * 2 + slot) * ROWS::kRows + r;
-                *reinterpret_cast<float2 *>(p.part_o + pr * D + c) = make_float2(a, b);
-                if (c == 0) p.part_ml[pr] = make_float2(m, l);
+                *reinterpret_cast<float4 *>(p.part_o + pr * D + c) = s.o;
+                if (c == 0) p.part_ml[pr] = make_float2(s.m, s.l);
             }
         }
         if (step == 0 && !whole && tid == 0) {
@@ -602,6 +648,14 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         }
         __syncthreads();                   // the next unit loads into the ring
     }
+}
+
+template <typename E> __device__ __forceinline__ void store2(void *p, size_t i, float a, float b);
+template <> __device__ __forceinline__ void store2<float>(void *p, size_t i, float a, float b) {
+    *reinterpret_cast<float2 *>(static_cast<float *>(p) + i) = make_float2(a, b);
+}
+template <> __device__ __forceinline__ void store2<__nv_bfloat16>(void *p, size_t i, float a, float b) {
+    *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + i) = pack2(a, b);
 }
 
 // Joins the parts of the units that more than one CTA ran: CTA (c, r) of this grid joins row r
@@ -734,8 +788,7 @@ cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int3
     p.list_len = list_len;
     p.recent = recent;
     p.window = window;
-    p.scale = scale;
-    p.cap = cap;
+    p.score = scoring(scale, cap);
     const bool bf16 = kv.dtype == GDN_BF16;
     if (kv.d == 128)
         return lists ? launch_dim<128, true>(p, bf16, workspace, stream)

@@ -73,15 +73,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// cap2 tanh(y) + add for |y| <= 1: tanh(y) = y R(y^2), R of degree 5 fitted to the least largest
-// relative error over [0, 1] (5.9e-7).
-__device__ __forceinline__ float2 capped_near2(float2 y, float cap2, float2 add) {
-    const float c[6] = {0.9999994136f * cap2, -0.3332904242f * cap2, 0.1328143402f * cap2,
-                        -0.0516056755f * cap2, 0.0167431149f * cap2, -0.0030670597f * cap2};
+// cap2 tanh(y) + add for |y| <= 1, by the polynomial
+__device__ __forceinline__ float2 capped_near_add2(float2 y, float cap2, float2 add) {
     const float2 t = mul2(y, y);
-    float2 r = make_float2(c[5], c[5]);
+    float2 r = make_float2(tanh_r(5) * cap2, tanh_r(5) * cap2);
 #pragma unroll
-    for (int i = 4; i >= 0; --i) r = fma2(r, t, make_float2(c[i], c[i]));
+    for (int i = 4; i >= 0; --i) r = fma2(r, t, make_float2(tanh_r(i) * cap2, tanh_r(i) * cap2));
     return fma2(y, r, add);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -204,8 +201,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int lo_max = see.lo(q0 + (i + 1) * bt_tile - 1), hi_min = see.hi(q0 + i * bt_tile);
         float m = -INFINITY, l = 0.f;                                    // m in base-2 units
         bool ok = true;
-        const float k2 = CAP ? fabsf(p.scale) * (2.f * kLog2e / p.cap) : p.scale2;
-        const float cap2 = p.cap * kLog2e, ky = CAP ? fabsf(p.scale) / p.cap : 0.f;
+        // |mul|: the products carry the scale's sign.  A scale of 0 makes every score equal, and so
+        // does 1e-30, which keeps -inf (a masked score) times it -inf.
+        const float k2 = CAP ? fabsf(p.score.mul) : fmaxf(fabsf(p.score.mul), 1e-30f);
+        const float cap2 = p.score.cap2;
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
             if (!__all_sync(0xffffffffu, wait(B_S + i, j))) { fail(1 + i); ok = false; break; }
@@ -229,11 +228,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     float far = 0.f;
 #pragma unroll
                     for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
-                    near = __all_sync(0xffffffffu, far * ky <= 1.f);
+                    near = __all_sync(0xffffffffu, far * k2 <= 1.f);
                 }
                 if (!near) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = capped2(s[c], k2, cap2);
+                    for (int c = 0; c < 128; ++c) s[c] = capped_exp2(s[c] * k2, cap2);
                 }
             }
             if (!whole) {
@@ -258,7 +257,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
             float mx = max3(fmaxf(mx4[0], s[124]), fmaxf(mx4[1], s[125]),
                             fmaxf(fmaxf(mx4[2], s[126]), fmaxf(mx4[3], s[127])));
-            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped2(mx, k2, cap2) : mx * k2;
+            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped_near2(mx * k2, cap2) : mx * k2;
             const bool grow = mx > m + kLazy;                            // also when m is -inf
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2(m - mx) : 1.f;                // 0 from -inf
@@ -309,7 +308,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tmem_st16(s_at + 48, w16);
             };
             if (CAP && near)
-                all_weights([&](float2 x) { return capped_near2(mul2(x, make_float2(ky, ky)), cap2, sh); });
+                all_weights([&](float2 x) { return capped_near_add2(mul2(x, make_float2(k2, k2)), cap2, sh); });
             else
                 all_weights([&](float2 x) { return fma2(x, kk, sh); });
             l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
@@ -356,7 +355,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             // Tile A's and tile B's turns alternate, which keeps the two softmax warpgroups half a period
             // apart (one issuing warp for each lets them fall into step).  The whole warp walks this code and one elected lane issues: descriptors then
             // stay in uniform registers (issued from a divergent thread, a product took 60-100 cycles).
-            const uint32_t neg = p.scale < 0.f ? 1u << 14 : 0u;          // the softmax takes |scale|
+            const uint32_t neg = p.score.mul < 0.f ? 1u << 14 : 0u;      // the softmax takes |mul|
             const uint32_t id_s = idesc_bf16(128, 128, false, false) | neg;
             const uint32_t id_o = idesc_bf16(128, D, false, true);
             const uint64_t q_desc = sdesc_kmajor(smem_u32(sm + L::kQ));
@@ -587,11 +586,7 @@ cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int
     p.window = window;
     // heads packed into a row tile: the largest power of two, up to 16, that divides the group
     while (p.pack_shift < 4 && p.G % (2 << p.pack_shift) == 0) ++p.pack_shift;
-    p.scale = scale;
-    // a scale of 0 makes every score equal; so does 1e-30, and -inf (a masked score) times it is
-    // still -inf
-    p.scale2 = fmaxf(fabsf(scale) * kLog2e, 1e-30f);
-    p.cap = cap;
+    p.score = scoring(scale, cap);
     p.err = static_cast<DeviceError *>(workspace);
     p.budget = budget;
     if (kv.dtype == GDN_F32) return launch_attn_prefill_f32(p, kv.d, stream);

@@ -4,6 +4,7 @@
 
 #include <math.h>
 
+#include "attn_math.cuh"
 #include "paged_kv.cuh"
 
 namespace gdn {
@@ -18,13 +19,10 @@ struct AttnPrefillParams {
     int N, H_q, G, window;
     bool heads_first;                      // order of the CTAs
     int pack_shift;                        // rows of a tile: token r >> pack_shift, head the rest
-    float scale2, cap;                     // |scale| log2 e; 0: no cap
-    float scale;
+    Scoring score;
     DeviceError *err;
     uint32_t budget;
 };
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Tokens {
     long long first;                       // row of the sequence's first token in q, out
@@ -110,20 +108,6 @@ __device__ __forceinline__ bool find_block(const AttnPrefillParams &p, F &&block
     n = found[0];
     b = found[1];
     return n >= 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// log2(e) cap tanh(dot scale / cap), with tanh(y) = 1 - 2 / (1 + e^{2y})
-__device__ __forceinline__ float capped2(float dot, float k, float cap2) {
-    return cap2 * (1.f - __fdividef(2.f, 1.f + ex2(dot * k)));
 }
 
 }  // namespace gdn

@@ -69,8 +69,6 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[a][d] = 0.f;
     }
-    const float k2 = p.cap > 0.f ? p.scale * (2.f * kLog2e / p.cap) : p.scale * kLog2e;
-    const float cap2 = p.cap * kLog2e;
     const float *kc = reinterpret_cast<const float *>(p.cache.k), *vc = reinterpret_cast<const float *>(p.cache.v);
     for (int k0 = k_lo; k0 < k_hi; k0 += kKeys) {
         __syncthreads();                                     // the last tile has been used
@@ -99,6 +97,7 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) s[a][b] = dot4(q[a], k[b], s[a][b]);
         }
+        score2(reinterpret_cast<float(&)[16]>(s), p.score);
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             float mx = m[a];
@@ -106,7 +105,7 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
             for (int b = 0; b < 4; ++b) {
                 const int key = tx + 16 * b;
                 const bool live = k0 + key >= lo[a] && k0 + key < hi[a] && rows[key] >= 0;
-                s[a][b] = !live ? -INFINITY : p.cap > 0.f ? capped2(s[a][b], k2, cap2) : s[a][b] * k2;
+                s[a][b] = live ? s[a][b] : -INFINITY;
                 mx = fmaxf(mx, s[a][b]);
             }
 #pragma unroll

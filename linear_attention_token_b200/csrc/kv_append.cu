@@ -5,9 +5,9 @@
 //   y[i + R/2]   = x[i + R/2] cos a + x[i] sin a,     a = position * inv_freq[i],  i < R/2
 //
 // Every element is read once and written once, so large calls are bound by HBM and small
-// ones by the latency of the dependent loads (offsets -> page table -> store).  A CTA takes
-// kTokens tokens; their angles' sines and cosines are formed once in shared memory and used
-// by every head, and the x loads are issued before that table is ready.
+// ones by the latency of the dependent loads (offsets -> page table -> store).  A warp takes a
+// token (or a share of one): it issues its first loads, forms the token's sines and cosines in
+// shared memory meanwhile, and uses them for every head.
 #include <math.h>
 #include <stdint.h>
 
@@ -18,8 +18,8 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;          // one warp finds one token's sequence and row
 constexpr int kMaxHalf = 64;           // largest rope_dims / 2
+constexpr int kFewWarps = 148 * 32;    // below this many warps a token is shared by several
 
 struct AppendParams {
     PagedView cache;
@@ -32,14 +32,16 @@ struct AppendParams {
     int num_seqs, H_q, half, n_axes;
     int sec[GDN_ROPE_MAX_AXES];
     bool interleaved;
+    int split_shift;                             // 2^split_shift warps share a token
 };
 
-// Angle p * f reduced to [-pi, pi] in double precision (a two-part 2 pi; Cody and Waite).  The
-// product of a 32-bit position and a 24-bit frequency loses at most its last bits in a double.
-__device__ __forceinline__ float turn(int p, float f) {
+// Angle p * f in half turns of pi, in [-1, 1]: the product of a 32-bit position and a 24-bit
+// frequency loses at most its last bits in a double, and is reduced there by a two-part 2 pi (Cody
+// and Waite).
+__device__ __forceinline__ float half_turns(int p, float f) {
     const double x = (double)p * (double)f;
     const double n = rint(x * 0.15915494309189535);
-    return (float)fma(-n, 2.4492935982947064e-16, fma(-n, 6.283185307179586, x));
+    return (float)(fma(-n, 2.4492935982947064e-16, fma(-n, 6.283185307179586, x)) * 0.3183098861837907);
 }
 
 __device__ __forceinline__ int axis_of(const AppendParams &p, int i) {
@@ -101,101 +103,121 @@ template <> struct Pack<__nv_bfloat16> {
     }
 };
 
-// One item is two 16-byte chunks of one head: a rotation pair, or two that pass through.
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int VEC = Pack<T>::kN, IPR = D / (2 * VEC);     // items per head
-    constexpr int BATCH = 4;                                  // items in flight per thread
-    __shared__ float2 trig[TOK][kMaxHalf];
-    __shared__ int row_of[TOK];                               // cache row, -1 absent, -2 no token
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long t0 = (long long)blockIdx.x * TOK;
-    const int heads = p.H_q + 2 * p.cache.H_kv;
-    const int per_token = heads * IPR, total = per_token * TOK;
+// A token's work is `heads` rows of D / (2 VEC) items; an item is two 16-byte chunks of one row: a
+// rotation pair, or two that pass through.  2^split_shift warps share a token's items; each forms
+// the token's sines and cosines for itself, so warps never wait for one another.
+// A lane has kBatch items (32 bytes each) in flight.  Many tokens: one, and 6 CTAs an SM (65,536
+// tokens x 20 rows: 113 us, 92% of the measured copy rate; 8 CTAs, which spill, 116; two items with
+// 5 CTAs 120, four with 3 130).  Few tokens: two, since nothing else hides the latency (3.5 against
+// 4.1 us for 64 tokens x 48 rows).
+template <typename T, int D, int kBatch>
+__global__ void __launch_bounds__(kThreads, kBatch == 1 ? 6 : 5) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int VEC = Pack<T>::kN, IPR = D / (2 * VEC);     // items per row
+    constexpr size_t ROW = (size_t)D * sizeof(T);
+    __shared__ float2 trig_of[kThreads / 32][kMaxHalf];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long gw = (long long)blockIdx.x * (kThreads / 32) + warp;
+    const long long t = gw >> p.split_shift;
+    if (t >= p.T_total) return;
+    float2 *trig = trig_of[warp];
+    const int H_q = p.H_q, H_k = p.cache.H_kv, total = (H_q + 2 * H_k) * IPR;
     const int pairs = p.half / VEC;
+    const int first = ((int)(gw & ((1 << p.split_shift) - 1)) << 5) + lane, step = 32 << p.split_shift;
 
-    if (warp < TOK) {
-        const long long t = t0 + warp;
-        int n = -1;
-        long long pos = 0;
-        if (t < p.T_total) {
-            n = p.cu ? sequence_of(p.cu, p.num_seqs, t) : (int)(t / p.T_seq);
-            if (n >= 0)
-                pos = t - (p.cu ? (long long)__ldg(p.cu + n) : n * p.T_seq) +
-                      (p.pos0 ? __ldg(p.pos0 + n) : 0);
-        }
-        if (lane == 0) row_of[warp] = n < 0 ? -2 : cache_row(p.cache, n, pos);
-        if (n >= 0)
-            for (int i = lane; i < p.half; i += 32) {
-                const int at = p.rope_pos ? __ldg(p.rope_pos + axis_of(p, i) * p.T_total + t)
-                                          : (int)pos;
-                float s, c;
-                sincosf(turn(at, __ldg(p.inv_freq + i)), &s, &c);
-                trig[warp][i] = make_float2(c, s);
-            }
-    }
-    for (int i0 = tid; i0 - tid < total; i0 += kThreads * BATCH) {       // uniform over the CTA
-        uint4 a[BATCH], b[BATCH];
+    // chunks and place of item i: q heads, then keys, then values
+    struct Item { int h, c0, c1; bool pair; };
+    auto item = [&](int i) {
+        Item x;
+        x.h = i / IPR;
+        const int j = i % IPR;
+        const bool value = x.h >= H_q + H_k;
+        x.pair = !value && j < pairs;
+        x.c0 = x.pair ? j : 2 * j;                           // (past the pairs: 2 pairs + 2 (j - pairs))
+        x.c1 = x.pair ? j + pairs : x.c0 + 1;
+        return x;
+    };
+    uint4 a[kBatch], b[kBatch];
+    auto load = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int i = i0 + u * kThreads;
-            const int tok = i / per_token, r = i - tok * per_token, h = r / IPR, j = r - h * IPR;
-            if (i >= total || t0 + tok >= p.T_total) continue;
-            const bool value = h >= p.H_q + p.cache.H_kv;
-            const bool pair = !value && j < pairs;
-            const unsigned char *src =
-                value ? p.v + (t0 + tok) * p.v_stride + (size_t)(h - p.H_q - p.cache.H_kv) * D * sizeof(T)
-                : h >= p.H_q ? p.k + (t0 + tok) * p.k_stride + (size_t)(h - p.H_q) * D * sizeof(T)
-                             : p.q + (t0 + tok) * p.q_stride + (size_t)h * D * sizeof(T);
-            const int c0 = pair ? j : value ? 2 * j : 2 * pairs + 2 * (j - pairs);
-            const int c1 = pair ? j + pairs : c0 + 1;
-            a[u] = *reinterpret_cast<const uint4 *>(src + c0 * 16);
-            b[u] = *reinterpret_cast<const uint4 *>(src + c1 * 16);
-        }
-        if (i0 == tid) __syncthreads();                     // the tables; the loads are in flight
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int i = i0 + u * kThreads;
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * step;
             if (i >= total) continue;
-            const int tok = i / per_token, r = i - tok * per_token, h = r / IPR, j = r - h * IPR;
-            const int row = row_of[tok];
-            if (row == -2 || (row < 0 && h >= p.H_q)) continue;
-            const bool value = h >= p.H_q + p.cache.H_kv;
-            const bool pair = !value && j < pairs;
-            if (pair) {
-                float x[VEC], y[VEC];
-                Pack<T>::get(a[u], x);
-                Pack<T>::get(b[u], y);
+            const Item x = item(i);
+            const unsigned char *src = x.h < H_q         ? p.q + t * p.q_stride + x.h * ROW
+                                       : x.h < H_q + H_k ? p.k + t * p.k_stride + (x.h - H_q) * ROW
+                                                         : p.v + t * p.v_stride + (x.h - H_q - H_k) * ROW;
+            a[u] = *reinterpret_cast<const uint4 *>(src + x.c0 * 16);
+            b[u] = *reinterpret_cast<const uint4 *>(src + x.c1 * 16);
+        }
+    };
+    load(first);                                             // in flight while the tables form
+
+    int n;
+    long long pos;
+    if (p.cu) {
+        n = sequence_of(p.cu, p.num_seqs, t);
+        if (n < 0) return;                                   // behind the last sequence
+        pos = t - __ldg(p.cu + n);
+    } else {
+        n = (int)(t / p.T_seq);
+        pos = t - n * p.T_seq;
+    }
+    if (p.pos0) pos += __ldg(p.pos0 + n);
+    const int row = cache_row(p.cache, n, pos);
+    for (int i = lane; i < p.half; i += 32) {
+        const int at = p.rope_pos ? __ldg(p.rope_pos + axis_of(p, i) * p.T_total + t) : (int)pos;
+        float s, c;
+        sincospif(half_turns(at, __ldg(p.inv_freq + i)), &s, &c);
+        trig[i] = make_float2(c, s);
+    }
+    __syncwarp();
+    for (int i0 = first; i0 < total;) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * step;
+            if (i >= total) continue;
+            const Item x = item(i);
+            if (row < 0 && x.h >= H_q) continue;             // absent: keys and values go nowhere
+            uint4 lo4 = a[u], hi4 = b[u];
+            if (x.pair) {
+                float lo[VEC], hi[VEC];
+                Pack<T>::get(lo4, lo);
+                Pack<T>::get(hi4, hi);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float2 cs = trig[tok][j * VEC + e];
-                    const float lo = x[e], hi = y[e];
-                    x[e] = lo * cs.x - hi * cs.y;
-                    y[e] = hi * cs.x + lo * cs.y;
+                    const float2 cs = trig[x.c0 * VEC + e];
+                    const float l = lo[e], h = hi[e];
+                    lo[e] = l * cs.x - h * cs.y;
+                    hi[e] = h * cs.x + l * cs.y;
                 }
-                a[u] = Pack<T>::put(x);
-                b[u] = Pack<T>::put(y);
+                lo4 = Pack<T>::put(lo);
+                hi4 = Pack<T>::put(hi);
             }
-            const int c0 = pair ? j : value ? 2 * j : 2 * pairs + 2 * (j - pairs);
-            const int c1 = pair ? j + pairs : c0 + 1;
-            const size_t head = (size_t)D * sizeof(T);
             unsigned char *dst =
-                value ? p.cache.v + ((size_t)row * p.cache.H_kv + (h - p.H_q - p.cache.H_kv)) * head
-                : h >= p.H_q ? p.cache.k + ((size_t)row * p.cache.H_kv + (h - p.H_q)) * head
-                             : p.q_out + ((size_t)(t0 + tok) * p.H_q + h) * head;
-            *reinterpret_cast<uint4 *>(dst + c0 * 16) = a[u];
-            *reinterpret_cast<uint4 *>(dst + c1 * 16) = b[u];
+                x.h < H_q         ? p.q_out + ((size_t)t * H_q + x.h) * ROW
+                : x.h < H_q + H_k ? p.cache.k + ((size_t)row * H_k + (x.h - H_q)) * ROW
+                                  : p.cache.v + ((size_t)row * H_k + (x.h - H_q - H_k)) * ROW;
+            *reinterpret_cast<uint4 *>(dst + x.c0 * 16) = lo4;
+            *reinterpret_cast<uint4 *>(dst + x.c1 * 16) = hi4;
         }
+        i0 += kBatch * step;
+        load(i0);
     }
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AppendParams &p, cudaStream_t stream) {
-    if (p.T_total < 2048)
-        kv_append_kernel<T, D, 1><<<(unsigned)p.T_total, kThreads, 0, stream>>>(p);
+cudaError_t launch_typed(AppendParams p, cudaStream_t stream) {
+    // warps per token: enough that a few tokens still spread over the SMs, no more than have items
+    const int items = (p.H_q + 2 * p.cache.H_kv) * D / (2 * Pack<T>::kN);
+    while (p.split_shift < 3 && (p.T_total << p.split_shift) < kFewWarps &&
+           (32 << p.split_shift) < items)
+        ++p.split_shift;
+    const long long warps = p.T_total << p.split_shift;
+    const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+    if (p.split_shift == 0)
+        kv_append_kernel<T, D, 1><<<grid, kThreads, 0, stream>>>(p);
     else
-        kv_append_kernel<T, D, kMaxTokens>
-            <<<(unsigned)((p.T_total + kMaxTokens - 1) / kMaxTokens), kThreads, 0, stream>>>(p);
+        kv_append_kernel<T, D, 2><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -40,6 +40,8 @@ __device__ __forceinline__ long long cache_capacity(const PagedView &c) {
     return (long long)c.max_pages << c.page_shift;
 }
 
+// Programmatic dependent launch: the join starts while the main kernel drains, and waits for its
+// completion (and its memory) before it reads anything.
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -151,6 +151,21 @@ def test_long_sequence_every_sm_joins():
     assert torch.equal(out, again) and torch.equal(lse, lse2)       # same order of sums
 
 
+def test_workspace_of_any_contents():
+    """One workspace for calls of different shapes in turn, whatever it holds."""
+    calls = []
+    for lens, T, H_q, H_kv in (([120_000], 1, 8, 1), ([700, 30], 4, 16, 2), ([9000] * 5, 1, 4, 4)):
+        q, pos, kv, _, _ = make(lens, T, H_q, H_kv, 128, 64, torch.bfloat16)
+        calls.append((q, pos, kv, gdn.gdn_attn_decode(q, pos, kv)))
+    n = max(gdn.gdn_attn_decode_workspace_size(q.shape[1], q.shape[2], kv.H_kv, 128)
+            for q, _, kv, _ in calls)
+    ws = torch.full((n,), 0xff, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        for q, pos, kv, (out, lse) in calls:
+            o, l = gdn.gdn_attn_decode(q, pos, kv, workspace=ws)
+            assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_peaked_scores():
     """Scores of hundreds, of both signs: one key decides, and the running maximum jumps."""
     q, pos, kv, ks, vs = make([2000], 1, 8, 2, 128, 16, torch.bfloat16, by=60.0)
