@@ -87,6 +87,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -139,22 +142,39 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bt_tile = kTile >> p.pack_shift, bt = 2 * bt_tile;        // tokens of a tile, block
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
+    // set up while the block's sequence is being found
+    if (warp == 8) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+    if (tid < 32 * 10 && tid >= 32 * 9) {
+        if (lane == 0) { prefetch_map(&tm_q); prefetch_map(&tm_k); prefetch_map(&tm_v); }
+        for (int b = lane; b < B_COUNT; b += 32) mbar_init(bars + b, b >= B_P && b < B_P + 4 ? 4 : 1);
+        if (lane == 0) *abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
     int n, blk;
+    Sequence seq;
     const int packs = p.G >> p.pack_shift, heads = p.cache.H_kv * packs;
     // Heads take turns when one head's blocks do not fill the SMs (so the longest blocks of all of
     // them start first: 442 against 474 us on 137 blocks x 4 heads), and follow one another when
     // they do (then all SMs read the same K and V: 126 against 130 us on 256 blocks x 2 heads).
     const int blocks = gridDim.x / heads;
     const int hx = p.heads_first ? blockIdx.x % heads : blockIdx.x / blocks;
-    if (!find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; },
-                              p.heads_first ? blockIdx.x / heads : blockIdx.x % blocks, n, blk))
+    const bool found = find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; },
+                                            p.heads_first ? blockIdx.x / heads : blockIdx.x % blocks, n, blk, seq);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (!found) {
+        if (warp == 8) tmem_dealloc(tmem, 512);
         return;
+    }
     const int hk = hx / packs;                                           // key head
     const int h0 = hk * p.G + (hx % packs << p.pack_shift);              // first query head
-    const Tokens seq = sequence_of(p, n);
     const long long first = seq.first;
     const int len = seq.len;
-    const Sight see(p, n, len);
+    const Sight see(p, seq);
     const int e = see.e;
     const int q0 = blk * bt;
     const int k_lo = see.lo(q0), k_base = k_lo / kTile * kTile;          // oldest token seen, its tile
@@ -165,19 +185,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     };
     const int tiles_a = tiles_of(0), tiles_b = tiles_of(1), nt = max(tiles_a, tiles_b);
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBars);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
-    if (warp == 8) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
-    if (tid == 0) {
-        for (int b = 0; b < B_COUNT; ++b) mbar_init(bars + b, b >= B_P && b < B_P + 4 ? 4 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     auto wait = [&](int b, int k) -> bool {                              // k-th completion of barrier b
         return wait_bounded(bars + b, (uint32_t)(k & 1), p.budget, abort_flag);
     };
@@ -320,31 +327,40 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         if (ok) {
             tc_fence_after();
-            // a thread's row: D values, in pieces of 32 (the TMEM loads are warp-wide)
+            // A thread's row goes through the tile's Q, which nobody reads any more (in the same
+            // swizzle), so that the warp stores whole rows: 16 bytes of 32 rows at a time cost 4,000
+            // cycles per CTA.
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const size_t rh = (size_t)(first + tok) * p.H_q + head;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + rh * D;
+            unsigned char *stage = sm + L::kQ + i * L::kTileBytes;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < (tiles > 0 ? D / 32 : 0); ++c) {
                 uint32_t o[32];
-                if (tiles > 0) {
-                    tmem_ld32(o_at + 32 * c, o);
-                    tmem_wait_ld();
-                } else {
+                tmem_ld32(o_at + 32 * c, o);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0;
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = pack2(__uint_as_float(o[8 * x + 2 * y]) * inv,
+                                     __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(stage + (c >> 1) * L::kHalf + sw128(row, 4 * (c & 1) + x)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (tok < len) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            w[y] = pack2(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                         __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * x) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+            }
+            __syncwarp();
+            constexpr int CH = D / 8, RPI = 32 / CH;                     // chunks of a row, rows at a time
+            const int ch = lane % CH;
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += RPI) {
+                const int r = 32 * (warp & 3) + r0 + lane / CH;
+                const int t = q0 + i * bt_tile + (r >> p.pack_shift), h = h0 + (r & ((1 << p.pack_shift) - 1));
+                const uint4 x = tiles > 0 ? *reinterpret_cast<const uint4 *>(stage + (ch >> 3) * L::kHalf + sw128(r, ch & 7))
+                                          : make_uint4(0, 0, 0, 0);
+                if (t < len)
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                               ((size_t)(first + t) * p.H_q + h) * D + 8 * ch) = x;
             }
             if (p.lse && tok < len) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }

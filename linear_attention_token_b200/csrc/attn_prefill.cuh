@@ -24,32 +24,36 @@ struct AttnPrefillParams {
     uint32_t budget;
 };
 
-struct Tokens {
-    long long first;                       // row of the sequence's first token in q, out
-    int len;
+// A sequence of the call: the row of its first token in q and out, its tokens, those cached before
+// them, and its prefix.
+struct Sequence {
+    long long first;
+    int len, start, pre;
 };
-// Tokens of sequence n, inside the call's T_total whatever the offsets say.
-__device__ __forceinline__ Tokens sequence_of(const AttnPrefillParams &p, int n) {
-    Tokens t;
+// Sequence n, inside the call's T_total tokens whatever the offsets say.
+__device__ __forceinline__ Sequence sequence_of(const AttnPrefillParams &p, int n) {
+    Sequence s;
+    s.start = p.pos0 ? __ldg(p.pos0 + n) : 0;
+    s.pre = p.prefix ? __ldg(p.prefix + n) : 0;
     if (!p.cu) {
-        t.first = n * p.T_seq;
-        t.len = (int)p.T_seq;
-        return t;
+        s.first = n * p.T_seq;
+        s.len = (int)p.T_seq;
+        return s;
     }
-    t.first = __ldg(p.cu + n);
+    s.first = __ldg(p.cu + n);
     const long long end = min((long long)__ldg(p.cu + n + 1), p.T_total);
-    t.len = t.first >= 0 && end > t.first ? (int)(end - t.first) : 0;
-    return t;
+    s.len = s.first >= 0 && end > s.first ? (int)(end - s.first) : 0;
+    return s;
 }
 
-// What the queries of sequence n see: query i sees the tokens [lo(i), hi(i)), both growing with i.
+// What the queries of a sequence see: query i sees the tokens [lo(i), hi(i)), both growing with i.
 struct Sight {
     long long start;
     int e, pre, window;
-    __device__ __forceinline__ Sight(const AttnPrefillParams &p, int n, int len) {
-        start = p.pos0 ? __ldg(p.pos0 + n) : 0;
-        e = (int)min(max(start + len, 0LL), cache_capacity(p.cache));
-        pre = p.prefix ? min(__ldg(p.prefix + n), e) : 0;
+    __device__ __forceinline__ Sight(const AttnPrefillParams &p, const Sequence &s) {
+        start = s.start;
+        e = (int)min(max(start + s.len, 0LL), cache_capacity(p.cache));
+        pre = min(s.pre, e);
         window = p.window;
     }
     __device__ __forceinline__ int hi(int i) const {
@@ -60,26 +64,34 @@ struct Sight {
     }
 };
 
-// Block x of the call: sequence n and its block b.  blocks_of(len) is a sequence's number of
-// blocks; they are numbered from the last one back, since a sequence's last blocks see the most
-// tokens and should start first.  All THREADS threads call it; false when x is past the last.
+// Block x of the call: its sequence (n, s) and its number b there.  blocks_of(len) is a sequence's
+// number of blocks; they are numbered from the last one back, since a sequence's last blocks see
+// the most tokens and should start first.  All THREADS threads call it, and it ends with a barrier;
+// false when x is past the last block.
 template <int THREADS, class F>
 __device__ __forceinline__ bool find_block(const AttnPrefillParams &p, F &&blocks_of, long long x,
-                                           int &n, int &b) {
+                                           int &n, int &b, Sequence &s) {
     __shared__ int sums[THREADS / 32], found[2];
+    __shared__ Sequence sequence;
     if (!p.cu) {
         const long long at = blocks_of(p.T_seq) * p.N - 1 - x;
-        if (at < 0) return false;
         b = (int)(at / p.N);               // the last blocks of all sequences first
         n = (int)(at % p.N);
-        return true;
+        if (at >= 0) s = sequence_of(p, n);
+        __syncthreads();
+        return at >= 0;
     }
-    // thread t counts the blocks of sequences [t per, t per + per)
+    // thread t counts the blocks of sequences [t per, t per + per); all that is needed of a
+    // sequence is loaded at once, so the search costs one trip to memory
     const int tid = threadIdx.x, per = (p.N + THREADS - 1) / THREADS;
     const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
     const int lane = tid & 31, warp = tid >> 5;
     int mine = 0;
-    for (int i = n0; i < n1; ++i) mine += (int)blocks_of(sequence_of(p, i).len);
+    s = Sequence{0, 0, 0, 0};
+    for (int i = n0; i < n1; ++i) {
+        s = sequence_of(p, i);
+        mine += (int)blocks_of(s.len);
+    }
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -97,16 +109,22 @@ __device__ __forceinline__ bool find_block(const AttnPrefillParams &p, F &&block
     }
     const int at = (int)(total - 1 - x);
     if (at >= before && at < before + mine) {
-        int left = at - before;
-        for (int i = n0; i < n1; ++i) {
-            const int nb = (int)blocks_of(sequence_of(p, i).len);
-            if (left < nb) { found[0] = i; found[1] = left; break; }
-            left -= nb;
-        }
+        int left = at - before, i = n0;
+        if (per > 1)
+            for (;; ++i) {
+                s = sequence_of(p, i);
+                const int nb = (int)blocks_of(s.len);
+                if (left < nb) break;
+                left -= nb;
+            }
+        found[0] = i;
+        found[1] = left;
+        sequence = s;
     }
     __syncthreads();
     n = found[0];
     b = found[1];
+    s = sequence;
     return n >= 0;
 }
 

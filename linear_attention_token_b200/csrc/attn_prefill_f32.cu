@@ -37,12 +37,12 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
     int *rows = reinterpret_cast<int *>(sm + L::kRow);       // cache row of each key, -1 absent
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     int n, blk;
+    Sequence seq;
     if (!find_block<kThreads>(p, [&](long long len) { return (len * p.G + kRows - 1) / kRows; },
-                              blockIdx.x, n, blk))
+                              blockIdx.x, n, blk, seq))
         return;
     const int hk = blockIdx.y;
-    const Tokens seq = sequence_of(p, n);
-    const Sight see(p, n, seq.len);
+    const Sight see(p, seq);
     const long long r0 = (long long)blk * kRows, r_end = (long long)seq.len * p.G;
     const int t_first = (int)(r0 / p.G), t_last = (int)((min(r0 + kRows, r_end) - 1) / p.G);
     const int k_lo = see.lo(t_first), k_hi = see.hi(t_last);
