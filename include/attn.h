@@ -123,7 +123,12 @@ gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos, const gdn_pa
                                int32_t H_q, float scale, float softcap, void *workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 
-/* Prompts.  Query i of sequence n sits at position p = pos0[n] + i; with e = pos0[n] plus the
+/* Bytes of device workspace that let gdn_attn_prefill use its fastest form for these sizes on the
+ * current device, at least 256; 0 for sizes it refuses.  varlen: nonzero when cu_seqlens is given.
+ * It depends on what the page table can hold, not on the lengths.  Calls that share a workspace
+ * must not overlap on the GPU.
+ *
+ * Prompts.  Query i of sequence n sits at position p = pos0[n] + i; with e = pos0[n] plus the
  * sequence's tokens in this call, it sees the tokens 0 <= t < e with t <= p, with window > 0
  * only those with t > p - window, and with prefix_len those with t < prefix_len[n] too (a
  * prefix that is seen both ways).
@@ -133,10 +138,14 @@ gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos, const gdn_pa
  *   pos0       : DEVICE int32[num_seqs] tokens cached before this call (>= 0), or NULL for 0
  *   prefix_len : DEVICE int32[num_seqs] or NULL; GDN_ERR_UNSUPPORTED together with a window
  *   lse        : [T_total, H_q] fp32 or NULL
- *   workspace  : at least 16 bytes of device memory whose first 16 hold the device error
- *                word (zero-filled before first use; gdn_get_device_error reads it), or NULL:
- *                a device-side timeout is then not reported.
+ *   workspace  : device memory whose first 16 bytes hold the device error word (zero-filled
+ *                before first use; gdn_get_device_error reads it), or NULL: a device-side
+ *                timeout is then not reported.  With gdn_attn_prefill_workspace_size bytes a
+ *                call of few query rows behind a long context is split over the context's
+ *                length (results differ by rounding); with less it runs in one piece.
  * Keys and values of the call's own tokens are in the cache already. */
+size_t gdn_attn_prefill_workspace_size(const gdn_paged_kv *kv, int32_t varlen, int32_t num_seqs,
+                                       int64_t T_total, int32_t H_q);
 gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv, const int32_t *cu_seqlens,
                             const int32_t *pos0, const int32_t *prefix_len, void *out,
                             float *lse, int32_t num_seqs, int64_t T_total, int32_t H_q,

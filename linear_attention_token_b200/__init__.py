@@ -17,7 +17,8 @@ from ._binding import (GDN_BF16, GDN_ERR_CUDA, GDN_ERR_INVALID_ARG, GDN_ERR_TIME
                        gdn_qsa_index_multi, gdn_qsa_index_multi_workspace_size,
                        qsa_index_multi_workspace, PagedKV, gdn_kv_append, rope_inv_freq,
                        gdn_attn_decode, gdn_qsa_attn_decode, gdn_attn_decode_workspace_size,
-                       attn_decode_workspace, gdn_attn_prefill)
+                       attn_decode_workspace, gdn_attn_prefill, gdn_attn_prefill_workspace_size,
+                       attn_prefill_workspace)
 
 __all__ = [
     "gdn_prefill", "gdn_prefill_static_scratch", "gdn_decode_step", "gdn_decode_multi", "gdn_backward", "gdn_get_device_error", "gdn_prefill_workspace_size",
@@ -29,5 +30,5 @@ __all__ = [
     "qsa_index_multi_workspace", "gdn_set_prefill_segment_tokens", "gdn_set_wait_budget",
     "gdn_prefill_schedule", "PagedKV", "gdn_kv_append", "rope_inv_freq", "gdn_attn_decode",
     "gdn_qsa_attn_decode", "gdn_attn_decode_workspace_size", "attn_decode_workspace",
-    "gdn_attn_prefill",
+    "gdn_attn_prefill", "gdn_attn_prefill_workspace_size", "attn_prefill_workspace",
 ]

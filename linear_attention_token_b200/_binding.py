@@ -39,7 +39,7 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_decode_step",
             "gdn_qsa_index_multi_workspace_size", "gdn_qsa_index_multi",
             "gdn_set_wait_budget", "gdn_set_prefill_segment_tokens", "gdn_prefill_schedule",
             "gdn_kv_append", "gdn_attn_decode_workspace_size", "gdn_attn_decode",
-            "gdn_qsa_attn_decode", "gdn_attn_prefill")
+            "gdn_qsa_attn_decode", "gdn_attn_prefill_workspace_size", "gdn_attn_prefill")
 
 _lib = None
 
@@ -114,6 +114,8 @@ def lib():
         L.gdn_qsa_attn_decode.argtypes = [P, P, KV, P, I32, I32, P, P, I32, I32, I32, F, F, P, SZ,
                                           P]
         L.gdn_qsa_attn_decode.restype = ctypes.c_int
+        L.gdn_attn_prefill_workspace_size.argtypes = [KV, I32, I32, I64, I32]
+        L.gdn_attn_prefill_workspace_size.restype = SZ
         L.gdn_attn_prefill.argtypes = [P, KV, P, P, P, P, P, I32, I64, I32, F, F, I32, P, SZ, P]
         L.gdn_attn_prefill.restype = ctypes.c_int
         L.gdn_get_device_error.argtypes = [P, P]
@@ -743,6 +745,21 @@ def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
     return out, lse
 
 
+def gdn_attn_prefill_workspace_size(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
+                                    varlen: bool = True) -> int:
+    return int(lib().gdn_attn_prefill_workspace_size(kv.ref, int(varlen), num_seqs, T_total, H_q))
+
+
+def attn_prefill_workspace(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
+                           varlen: bool = True) -> torch.Tensor:
+    """A workspace for gdn_attn_prefill calls of these sizes, its error word zero-filled.  Calls
+    that may overlap on the GPU need one each."""
+    n = gdn_attn_prefill_workspace_size(kv, num_seqs, T_total, H_q, varlen)
+    workspace = torch.empty(n, dtype=torch.uint8, device=kv.device)
+    workspace[:256].zero_()
+    return workspace
+
+
 @_placed
 def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=None,
                      scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, out=None,
@@ -750,9 +767,9 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
     """Attention of prompts whose keys and values are in the cache already: q [T_total, H_q, d]
     with cu_seqlens int32 [N + 1], or [B, T, H_q, d]; query i of sequence n sits at position
     pos0[n] + i (pos0 None: 0) and sees the tokens at or before it, with window > 0 only the last
-    `window` of them, with prefix_len int32 [N] also those before prefix_len[n].  A workspace (16
-    zero-filled bytes or more) records a device-side timeout for gdn_get_device_error.  Returns
-    (out, lse [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are
+    `window` of them, with prefix_len int32 [N] also those before prefix_len[n].  A workspace
+    (attn_prefill_workspace; None takes one for the call) records a device-side timeout for
+    gdn_get_device_error and lets few rows behind a long context use all SMs.  Returns (out, lse [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are
     left alone."""
     T_total, N = _sequences(q, cu_seqlens, kv)
     if q.shape[-1] != kv.d:
@@ -764,6 +781,10 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
     if lse is None and want_lse:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
     wp, wn = None, 0
+    if workspace is None and kv.index >= 0:
+        wn = lib().gdn_attn_prefill_workspace_size(kv.ref, cu_seqlens is not None, N, T_total, H_q)
+        if wn > 256:                              # 256: only the error word, which nobody would read
+            workspace = torch.empty(wn, dtype=torch.uint8, device=dev)
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}")

@@ -65,8 +65,11 @@ cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int3
                                float cap, int window, void *workspace, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
                                 const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
-                                int N, long long T_total, int H_q, float scale, float cap,
-                                int window, void *workspace, uint32_t budget, cudaStream_t stream);
+                                int N, long long T_total, int H_q, float scale, float cap, int window,
+                                void *workspace, size_t workspace_bytes, int sms, uint32_t budget,
+                                cudaStream_t stream);
+size_t attn_prefill_workspace_bytes(const gdn_paged_kv &kv, bool varlen, int N, long long T_total, int H_q,
+                                    int sms);
 size_t static_scratch_capacity();
 cudaError_t static_scratch_ptr(void **out);
 }  // namespace gdn
@@ -499,6 +502,11 @@ gdn_status paged_checks(const gdn_paged_kv *kv, int32_t num_seqs)
     return GDN_OK;
 }
 
+int sm_count()
+{
+    const int sms = gdn::device_sm_count();
+    return sms > 0 ? sms : kDefaultSms;
+}
 bool softcap_ok(float cap) { return cap >= 0.f && cap < INFINITY; }
 bool scale_ok(float scale) { return scale > -INFINITY && scale < INFINITY; }
 }  // namespace
@@ -553,9 +561,7 @@ GDN_API size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, in
         H_q % H_kv != 0 || H_q > kMostHeads || !head_dim_ok(d) ||
         (dtype != GDN_F32 && dtype != GDN_BF16))
         return 0;
-    int sms = gdn::device_sm_count();
-    if (sms <= 0) sms = kDefaultSms;
-    return gdn::attn_decode_workspace_bytes(H_q / H_kv * n_queries, d, sms);
+    return gdn::attn_decode_workspace_bytes(H_q / H_kv * n_queries, d, sm_count());
 }
 
 namespace {
@@ -612,6 +618,16 @@ GDN_API gdn_status gdn_qsa_attn_decode(const void *q, const int32_t *q_pos,
                        n_queries, H_q, scale, softcap, 0, workspace, workspace_bytes, stream);
 }
 
+GDN_API size_t gdn_attn_prefill_workspace_size(const gdn_paged_kv *kv, int32_t varlen, int32_t num_seqs,
+                                               int64_t T_total, int32_t H_q)
+{
+    if (paged_checks(kv, num_seqs) != GDN_OK || T_total < 0 || T_total > INT32_MAX || H_q <= 0 ||
+        H_q % kv->H_kv != 0 || H_q > kMostHeads || (!varlen && T_total > 0 && (num_seqs == 0 || T_total % num_seqs != 0)))
+        return 0;
+    if (T_total == 0 || num_seqs == 0) return kWorkspaceBytes;
+    return gdn::attn_prefill_workspace_bytes(*kv, varlen != 0, num_seqs, T_total, H_q, sm_count());
+}
+
 GDN_API gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv,
                                     const int32_t *cu_seqlens, const int32_t *pos0,
                                     const int32_t *prefix_len, void *out, float *lse,
@@ -636,7 +652,8 @@ GDN_API gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv,
     if (workspace && workspace_bytes < sizeof(gdn::DeviceError)) return GDN_ERR_INVALID_ARG;
     const cudaError_t e = gdn::launch_attn_prefill(*kv, q, cu_seqlens, pos0, prefix_len, out, lse,
                                                    num_seqs, T_total, H_q, scale, softcap, window,
-                                                   workspace, g_wait_budget.load(), stream);
+                                                   workspace, workspace_bytes, sm_count(),
+                                                   g_wait_budget.load(), stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -21,12 +21,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// tanh(y) = y R(y^2) on |y| <= 1: R of degree 5 fitted to the least largest relative error over
-// [0, 1] (5.9e-7).
+// tanh(y) = y R(y^2), R fitted to the least largest relative error: of degree 5 for |y| <= 1 (5.9e-7),
+// of degree 3 for |y| <= 1/2 (5.5e-7).
+template <int DEG>
 __device__ constexpr float tanh_r(int i) {
-    constexpr float c[6] = {0.9999994136f, -0.3332904242f, 0.1328143402f,
-                            -0.0516056755f, 0.0167431149f, -0.0030670597f};
-    return c[i];
+    constexpr float c5[6] = {0.9999994136f, -0.3332904242f, 0.1328143402f,
+                             -0.0516056755f, 0.0167431149f, -0.0030670597f};
+    constexpr float c3[4] = {0.9999994636f, -0.3332631886f, 0.1319029629f, -0.0444022268f};
+    return DEG == 5 ? c5[i] : c3[i & 3];
 }
 
 // What turns a dot product into a score: scale alone, or scale and cap.
@@ -47,9 +49,9 @@ __device__ __forceinline__ float capped_exp2(float y, float cap2) {
 // cap2 tanh(y) for |y| <= 1, by the polynomial: off by a few 2^-24 of itself
 __device__ __forceinline__ float capped_near2(float y, float cap2) {
     const float t = y * y;
-    float r = tanh_r(5);
+    float r = tanh_r<5>(5);
 #pragma unroll
-    for (int i = 4; i >= 0; --i) r = fmaf(r, t, tanh_r(i));
+    for (int i = 4; i >= 0; --i) r = fmaf(r, t, tanh_r<5>(i));
     return cap2 * (y * r);
 }
 // N dot products of each lane to scores, in place; the warp takes the polynomial when none of its

@@ -45,7 +45,7 @@ constexpr int kThreads = 384, kSlots = 4, kMaskRing = 8;
 // Registers a thread: 168 at launch (384 threads); the softmax warps, which hold a row of scores,
 // take what the third warpgroup gives up: 2 x 208 + 88 = 3 x 168.
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
-constexpr int kTile = 128;                 // query rows of a tile, tokens of a K / V tile
+constexpr int kTile = kPrefillTile;        // query rows of a tile, tokens of a K / V tile
 constexpr uint32_t kPollNs = 2000, kDrainBudget = GDN_DEFAULT_WAIT_BUDGET;
 constexpr float kLazy = 8.f;               // growth of a row maximum (base 2) that O may lag
 
@@ -73,12 +73,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// cap2 tanh(y) + add for |y| <= 1, by the polynomial
+// cap2 tanh(y) + add, by the polynomial of degree DEG
+template <int DEG>
 __device__ __forceinline__ float2 capped_near_add2(float2 y, float cap2, float2 add) {
     const float2 t = mul2(y, y);
-    float2 r = make_float2(tanh_r(5) * cap2, tanh_r(5) * cap2);
+    float2 r = make_float2(tanh_r<DEG>(DEG) * cap2, tanh_r<DEG>(DEG) * cap2);
 #pragma unroll
-    for (int i = 4; i >= 0; --i) r = fma2(r, t, make_float2(tanh_r(i) * cap2, tanh_r(i) * cap2));
+    for (int i = DEG - 1; i >= 0; --i)
+        r = fma2(r, t, make_float2(tanh_r<DEG>(i) * cap2, tanh_r<DEG>(i) * cap2));
     return fma2(y, r, add);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -131,6 +133,13 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uin
     return false;
 }
 
+// What the outputs need of a block, kept in shared memory while the registers hold scores.
+struct Outputs {
+    long long first;                       // row of the sequence's first token
+    int len, q0, h0;                       // its tokens; the block's first token and query head
+    int parts, part;                       // CTAs that share the block; this one's place among all parts
+};
+
 template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -140,6 +149,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Outputs block_outputs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bt_tile = kTile >> p.pack_shift, bt = 2 * bt_tile;        // tokens of a tile, block
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBars);
@@ -154,19 +164,21 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         fence_mbar_init();
     }
     tc_fence_before();
+    pdl_trigger();
     int n, blk;
     Sequence seq;
     const int packs = p.G >> p.pack_shift, heads = p.cache.H_kv * packs;
     // Heads take turns when one head's blocks do not fill the SMs (so the longest blocks of all of
     // them start first: 442 against 474 us on 137 blocks x 4 heads), and follow one another when
     // they do (then all SMs read the same K and V: 126 against 130 us on 256 blocks x 2 heads).
-    const int blocks = gridDim.x / heads;
-    const int hx = p.heads_first ? blockIdx.x % heads : blockIdx.x / blocks;
+    const int block = blockIdx.x / p.splits, split = blockIdx.x % p.splits, blocks = gridDim.x / p.splits / heads;
+    const int hx = p.heads_first ? block % heads : block / blocks;
     const bool found = find_block<kThreads>(p, [&](long long len) { return (len + bt - 1) / bt; },
-                                            p.heads_first ? blockIdx.x / heads : blockIdx.x % blocks, n, blk, seq);
+                                            p.heads_first ? block / heads : block % blocks, n, blk, seq);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (!found) {
+        if (p.splits > 1 && split == 0 && tid == 0) p.split_blocks[block].parts = 0;
         if (warp == 8) tmem_dealloc(tmem, 512);
         return;
     }
@@ -177,14 +189,33 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const Sight see(p, seq);
     const int e = see.e;
     const int q0 = blk * bt;
-    const int k_lo = see.lo(q0), k_base = k_lo / kTile * kTile;          // oldest token seen, its tile
+    const int k_lo = see.lo(q0);                                         // oldest token seen
+    int k_base = k_lo / kTile * kTile;
     auto tiles_of = [&](int i) -> int {                                  // K / V tiles row tile i walks
         const int a = q0 + i * bt_tile;
         const int hi = a < len ? see.hi(min(a + bt_tile, len) - 1) : 0;
         return hi > k_base ? (hi - k_base + kTile - 1) / kTile : 0;
     };
-    const int tiles_a = tiles_of(0), tiles_b = tiles_of(1), nt = max(tiles_a, tiles_b);
+    int tiles_a = tiles_of(0), tiles_b = tiles_of(1), nt = max(tiles_a, tiles_b);
+    int parts = 1;
+    if (p.splits > 1) {
+        parts = split_parts(nt, p.splits);
+        if (split == 0 && tid == 0)
+            p.split_blocks[block] = SplitBlock{first, len, q0 << p.pack_shift, 1 << p.pack_shift, h0, parts, 0};
+        if (split >= parts) {
+            if (warp == 8) tmem_dealloc(tmem, 512);
+            return;
+        }
+        int from, to;
+        split_range(nt, parts, split, from, to);
+        k_base += from * kTile;
+        nt = to - from;
+        tiles_a = min(max(tiles_a - from, 0), nt);
+        tiles_b = min(max(tiles_b - from, 0), nt);
+    }
 
+    if (tid == 0) block_outputs = Outputs{first, len, q0, h0, parts, block * p.splits + split};
+    __syncthreads();
     auto wait = [&](int b, int k) -> bool {                              // k-th completion of barrier b
         return wait_bounded(bars + b, (uint32_t)(k & 1), p.budget, abort_flag);
     };
@@ -202,7 +233,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + kTmS + 128 * i, o_at = tmem + lanes + kTmO + 128 * i;
         const int tok = q0 + i * bt_tile + (row >> p.pack_shift);
-        const int head = h0 + (row & ((1 << p.pack_shift) - 1));
         const int lo = see.lo(tok), hi = see.hi(tok);
         // tiles that every row of this row tile sees whole
         const int lo_max = see.lo(q0 + (i + 1) * bt_tile - 1), hi_min = see.hi(q0 + i * bt_tile);
@@ -227,15 +257,17 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
             const bool whole = k0 >= lo_max && k0 + kTile <= hi_min &&
                                (pm.x & pm.y & pm.z & pm.w) == 0xffffffffu;
-            // tanh(y) = y R(y^2) on the FMA pipe while no score of the warp's rows passes the cap
-            // (|y| <= 1), else by exponentials (two more per score on the busiest pipe)
-            bool near = false;
+            // tanh(y) by a polynomial on the FMA pipe while no score of the warp's rows passes the
+            // cap (|y| <= 1), a shorter one while none passes half of it, else by exponentials (two
+            // more per score on the busiest pipe)
+            bool near = false, nearer = false;
             if (CAP) {
                 if (whole) {
                     float far = 0.f;
 #pragma unroll
                     for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
                     near = __all_sync(0xffffffffu, far * k2 <= 1.f);
+                    nearer = __all_sync(0xffffffffu, far * k2 <= 0.5f);
                 }
                 if (!near) {
 #pragma unroll
@@ -314,8 +346,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 for (int x = 0; x < 16; ++x) w16[x] = weights(96 + 2 * x);
                 tmem_st16(s_at + 48, w16);
             };
-            if (CAP && near)
-                all_weights([&](float2 x) { return capped_near_add2(mul2(x, make_float2(k2, k2)), cap2, sh); });
+            if (CAP && nearer)
+                all_weights([&](float2 x) { return capped_near_add2<3>(mul2(x, make_float2(k2, k2)), cap2, sh); });
+            else if (CAP && near)
+                all_weights([&](float2 x) { return capped_near_add2<5>(mul2(x, make_float2(k2, k2)), cap2, sh); });
             else
                 all_weights([&](float2 x) { return fma2(x, kk, sh); });
             l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
@@ -327,42 +361,62 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         if (ok) {
             tc_fence_after();
-            // A thread's row goes through the tile's Q, which nobody reads any more (in the same
-            // swizzle), so that the warp stores whole rows: 16 bytes of 32 rows at a time cost 4,000
-            // cycles per CTA.
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const size_t rh = (size_t)(first + tok) * p.H_q + head;
-            unsigned char *stage = sm + L::kQ + i * L::kTileBytes;
+            const volatile Outputs &to = block_outputs;
+            const long long first_row = to.first;
+            const int tokens = to.len, token0 = to.q0 + i * bt_tile, head0 = to.h0, pack_mask = (1 << p.pack_shift) - 1;
+            if (to.parts > 1) {
+                // this CTA's share: unnormalised, in fp32 (a thread writes 128 bytes at a time)
+                const size_t at = (size_t)to.part * 2 * kTile + i * kTile + row;
+                p.part_ml[at] = make_float2(m, l);
 #pragma unroll 1
-            for (int c = 0; c < (tiles > 0 ? D / 32 : 0); ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_at + 32 * c, o);
-                tmem_wait_ld();
+                for (int c = 0; c < (tiles > 0 ? D / 32 : 0); ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + 32 * c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        w[y] = pack2(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                     __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(stage + (c >> 1) * L::kHalf + sw128(row, 4 * (c & 1) + x)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * c + 4 * x) =
+                            make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                 }
-            }
-            __syncwarp();
-            constexpr int CH = D / 8, RPI = 32 / CH;                     // chunks of a row, rows at a time
-            const int ch = lane % CH;
+            } else {
+                // A thread's row goes through the tile's Q, which nobody reads any more (in the same
+                // swizzle), so that the warp stores whole rows.
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                unsigned char *stage = sm + L::kQ + i * L::kTileBytes;
+#pragma unroll 1
+                for (int c = 0; c < (tiles > 0 ? D / 32 : 0); ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = pack2(__uint_as_float(o[8 * x + 2 * y]) * inv,
+                                         __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(stage + (c >> 1) * L::kHalf + sw128(row, 4 * (c & 1) + x)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncwarp();
+                constexpr int CH = D / 8, RPI = 32 / CH;                 // chunks of a row, rows at a time
+                const int ch = lane % CH;
 #pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += RPI) {
-                const int r = 32 * (warp & 3) + r0 + lane / CH;
-                const int t = q0 + i * bt_tile + (r >> p.pack_shift), h = h0 + (r & ((1 << p.pack_shift) - 1));
-                const uint4 x = tiles > 0 ? *reinterpret_cast<const uint4 *>(stage + (ch >> 3) * L::kHalf + sw128(r, ch & 7))
-                                          : make_uint4(0, 0, 0, 0);
-                if (t < len)
-                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                               ((size_t)(first + t) * p.H_q + h) * D + 8 * ch) = x;
+                for (int r0 = 0; r0 < 32; r0 += RPI) {
+                    const int r = 32 * (warp & 3) + r0 + lane / CH;
+                    const int t = token0 + (r >> p.pack_shift), h = head0 + (r & pack_mask);
+                    const uint4 x = tiles > 0 ? *reinterpret_cast<const uint4 *>(stage + (ch >> 3) * L::kHalf + sw128(r, ch & 7))
+                                              : make_uint4(0, 0, 0, 0);
+                    if (t < tokens)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                   ((size_t)(first_row + t) * p.H_q + h) * D + 8 * ch) = x;
+                }
+                const int t = token0 + (row >> p.pack_shift);
+                if (p.lse && t < tokens)
+                    p.lse[(size_t)(first_row + t) * p.H_q + head0 + (row & pack_mask)] =
+                        l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
-            if (p.lse && tok < len) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
     } else {
         regs_give<kRegsOther>();
@@ -553,7 +607,7 @@ bool make_map(CUtensorMap *map, const void *base, long long rows, int heads, int
 template <int D, bool CAP> PerDevice g_setup;
 
 template <int D, bool CAP>
-cudaError_t launch_tc(AttnPrefillParams p, const gdn_paged_kv &kv, cudaStream_t stream) {
+cudaError_t launch_dim(AttnPrefillParams p, const gdn_paged_kv &kv, cudaStream_t stream) {
     constexpr int smem = Smem<D>::kTotal;
     int sms = 0;
     cudaError_t e = g_setup<D, CAP>.ensure([] {
@@ -561,7 +615,7 @@ cudaError_t launch_tc(AttnPrefillParams p, const gdn_paged_kv &kv, cudaStream_t 
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     }, &sms);
     if (e != cudaSuccess) return e;
-    const int pack = 1 << p.pack_shift, bt = 2 * (kTile >> p.pack_shift);
+    const int pack = 1 << p.pack_shift;
     const int box = kv.page_size < kTile ? kv.page_size : kTile;
     const long long rows = (long long)kv.num_pages * kv.page_size;
     CUtensorMap mq, mk, mv;
@@ -569,46 +623,17 @@ cudaError_t launch_tc(AttnPrefillParams p, const gdn_paged_kv &kv, cudaStream_t 
         !make_map(&mk, kv.k, rows, kv.H_kv, D, 1, box) ||
         !make_map(&mv, kv.v, rows, kv.H_kv, D, 1, box))
         return cudaErrorInvalidValue;
-    // at most one block per sequence is not full
-    const long long blocks = p.cu ? p.T_total / bt + p.N : (p.T_seq + bt - 1) / bt * p.N;
-    const long long grid = blocks * kv.H_kv * (p.G >> p.pack_shift);
-    p.heads_first = blocks < sms;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    attn_prefill_kernel<D, CAP><<<(unsigned)grid, kThreads, smem, stream>>>(mq, mk, mv, p);
+    p.heads_first = p.blocks / (kv.H_kv * (p.G >> p.pack_shift)) < sms;
+    attn_prefill_kernel<D, CAP><<<(unsigned)(p.blocks * p.splits), kThreads, smem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefill_f32(const AttnPrefillParams &p, int d, cudaStream_t stream);
-
-cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
-                                const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
-                                int N, long long T_total, int H_q, float scale, float cap,
-                                int window, void *workspace, uint32_t budget, cudaStream_t stream) {
-    AttnPrefillParams p = {};
-    p.cache = paged_view(kv);
-    p.q = q;
-    p.out = out;
-    p.lse = lse;
-    p.cu = cu;
-    p.pos0 = pos0;
-    p.prefix = prefix;
-    p.T_total = T_total;
-    p.T_seq = cu ? 0 : T_total / N;
-    p.N = N;
-    p.H_q = H_q;
-    p.G = H_q / kv.H_kv;
-    p.window = window;
-    // heads packed into a row tile: the largest power of two, up to 16, that divides the group
-    while (p.pack_shift < 4 && p.G % (2 << p.pack_shift) == 0) ++p.pack_shift;
-    p.score = scoring(scale, cap);
-    p.err = static_cast<DeviceError *>(workspace);
-    p.budget = budget;
-    if (kv.dtype == GDN_F32) return launch_attn_prefill_f32(p, kv.d, stream);
-    if (kv.d == 128)
-        return cap > 0.f ? launch_tc<128, true>(p, kv, stream) : launch_tc<128, false>(p, kv, stream);
-    return cap > 0.f ? launch_tc<64, true>(p, kv, stream) : launch_tc<64, false>(p, kv, stream);
+cudaError_t launch_attn_prefill_bf16(const AttnPrefillParams &p, const gdn_paged_kv &kv, cudaStream_t stream) {
+    const bool cap = p.score.cap2 != 0.f;
+    if (kv.d == 128) return cap ? launch_dim<128, true>(p, kv, stream) : launch_dim<128, false>(p, kv, stream);
+    return cap ? launch_dim<64, true>(p, kv, stream) : launch_dim<64, false>(p, kv, stream);
 }
 
 }  // namespace gdn

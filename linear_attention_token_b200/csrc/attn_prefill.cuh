@@ -22,8 +22,40 @@ struct AttnPrefillParams {
     Scoring score;
     DeviceError *err;
     uint32_t budget;
+    long long blocks;                      // (block, head) pairs, as prefill_shape counts them
+    // A long context with few blocks: `splits` CTAs share a block's tokens, and their parts (of
+    // part_rows rows, m and l, and unnormalised outputs) are joined by attn_prefill_join_kernel.
+    int splits;                            // 1: none
+    struct SplitBlock *split_blocks;       // [blocks x heads]
+    float2 *part_ml;                       // [blocks x heads, splits, part_rows]
+    float *part_o;                         // [.., d]
 };
 
+// What a split block's first CTA leaves for the join.  Row r of the block is token
+// (row0 + r) / pack of the sequence and head h0 + (row0 + r) % pack.
+struct SplitBlock {
+    long long first;
+    int len, row0, pack, h0;
+    int parts;                             // CTAs that took a share (0 or 1: nothing to join)
+    int pad;
+};
+
+// How the two kernels cut a call (their CTAs' query rows and K / V tiles).
+constexpr int kPrefillTile = 128, kPrefillRows = 2 * kPrefillTile;             // bf16
+constexpr int kF32Rows = 64, kF32Keys = 64;                                    // fp32
+
+// Least K / V tiles that are worth a CTA of their own (16 rows behind 2048 tokens: 18.8 us with 3, 19.6
+// with 4, 26 with 8, 35 in one piece; 300 x 2 x 8 rows behind 1024: 24, 26, 28, 28).
+constexpr int kSplitTiles = 3;
+
+// CTAs that share a block's `tiles`, and the share of CTA s: tiles [from, to).
+__device__ __forceinline__ int split_parts(int tiles, int splits) {
+    return max(1, min(splits, tiles / kSplitTiles));
+}
+__device__ __forceinline__ void split_range(int tiles, int parts, int s, int &from, int &to) {
+    from = (int)((long long)tiles * s / parts);
+    to = (int)((long long)tiles * (s + 1) / parts);
+}
 // A sequence of the call: the row of its first token in q and out, its tokens, those cached before
 // them, and its prefix.
 struct Sequence {

@@ -14,7 +14,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256, kRows = 64, kKeys = 64;
+constexpr int kThreads = 256, kRows = kF32Rows, kKeys = kF32Keys;
 
 template <int D>
 struct Smem {
@@ -36,16 +36,31 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
     float *sq = sm + L::kQ, *sk = sm + L::kK, *sv = sm + L::kV, *sp = sm + L::kP;
     int *rows = reinterpret_cast<int *>(sm + L::kRow);       // cache row of each key, -1 absent
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    pdl_trigger();
+    const int block = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const int hk = block % p.cache.H_kv;
     int n, blk;
     Sequence seq;
     if (!find_block<kThreads>(p, [&](long long len) { return (len * p.G + kRows - 1) / kRows; },
-                              blockIdx.x, n, blk, seq))
+                              block / p.cache.H_kv, n, blk, seq)) {
+        if (p.splits > 1 && split == 0 && tid == 0) p.split_blocks[block].parts = 0;
         return;
-    const int hk = blockIdx.y;
+    }
     const Sight see(p, seq);
     const long long r0 = (long long)blk * kRows, r_end = (long long)seq.len * p.G;
     const int t_first = (int)(r0 / p.G), t_last = (int)((min(r0 + kRows, r_end) - 1) / p.G);
-    const int k_lo = see.lo(t_first), k_hi = see.hi(t_last);
+    int k_lo = see.lo(t_first), k_hi = see.hi(t_last), parts = 1;
+    if (p.splits > 1) {
+        const int tiles = k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0;
+        parts = split_parts(tiles, p.splits);
+        if (split == 0 && tid == 0)
+            p.split_blocks[block] = SplitBlock{seq.first, seq.len, blk * kRows, p.G, hk * p.G, parts, 0};
+        if (split >= parts) return;
+        int from, to;
+        split_range(tiles, parts, split, from, to);
+        k_hi = min(k_hi, k_lo + to * kKeys);
+        k_lo += from * kKeys;
+    }
     auto row_at = [&](long long r) -> size_t {
         return (size_t)(seq.first + r / p.G) * p.H_q + (size_t)hk * p.G + r % p.G;
     };
@@ -153,6 +168,15 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
         for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const long long r = r0 + 4 * ty + a;
         if (r >= r_end) continue;
+        if (parts > 1) {                                     // this CTA's share, unnormalised
+            const size_t part = ((size_t)block * p.splits + split) * kRows + 4 * ty + a;
+            if (tx == 0) p.part_ml[part] = make_float2(m[a], sum);
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+                *reinterpret_cast<float4 *>(p.part_o + part * D + 64 * d + 4 * tx) =
+                    make_float4(o[a][4 * d], o[a][4 * d + 1], o[a][4 * d + 2], o[a][4 * d + 3]);
+            continue;
+        }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const size_t at = row_at(r);
 #pragma unroll
@@ -172,10 +196,7 @@ cudaError_t launch_dim(const AttnPrefillParams &p, cudaStream_t stream) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     });
     if (e != cudaSuccess) return e;
-    const long long blocks = p.cu ? p.T_total * p.G / kRows + p.N : (p.T_seq * p.G + kRows - 1) / kRows * p.N;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    attn_prefill_f32_kernel<D><<<dim3((unsigned)blocks, (unsigned)p.cache.H_kv), kThreads,
-                                 Smem<D>::kBytes, stream>>>(p);
+    attn_prefill_f32_kernel<D><<<(unsigned)(p.blocks * p.splits), kThreads, Smem<D>::kBytes, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -88,9 +88,61 @@ def test_matches_definition(lens, past, H_q, H_kv, d, page, softcap, window, pre
            lambda n: seen_by(lens[n], past[n], window, prefix[n] if prefix else 0))
     assert bool((out[sum(lens):] == 7.0).all()) and bool((lse[sum(lens):] == 7.0).all())
     again, lse2 = gdn.gdn_attn_prefill(q, kv, cu, pos0, prefix_len=pre, softcap=softcap,
-                                       window=window)
+                                       window=window, workspace=ws)
     assert torch.equal(again[:sum(lens)], out[:sum(lens)])  # same order of sums
     assert torch.equal(lse2[:sum(lens)], lse[:sum(lens)])
+
+
+SPLIT_CASES = [
+    # lens, past, H_q, H_kv, d, page, softcap, window, prefix, dtype
+    ([64], [5000], 16, 2, 128, 64, 0.0, 0, None, BF),
+    ([3, 40, 1, 0], [9000, 100, 2500, 3], 8, 1, 128, 16, 0.0, 0, None, BF),
+    ([70], [9000], 3, 1, 64, 128, 20.0, 0, None, BF),
+    ([40, 9], [9000, 4000], 8, 2, 128, 16, 0.0, 3000, None, BF),
+    ([33, 9], [3000, 6000], 4, 1, 128, 64, 0.0, 0, [3020, 10], BF),
+    ([100], [4000], 8, 2, 128, 64, 0.0, 0, None, F32),
+    ([9, 0, 50], [4000, 9, 600], 6, 1, 64, 16, 10.0, 0, None, F32),
+    ([9, 50], [4000, 3000], 2, 2, 64, 16, 0.0, 2000, None, F32),
+]
+
+
+@pytest.mark.parametrize("lens,past,H_q,H_kv,d,page,softcap,window,prefix,dtype", SPLIT_CASES)
+def test_few_rows_behind_a_long_context(lens, past, H_q, H_kv, d, page, softcap, window, prefix, dtype):
+    """Calls that are split over the context's length, and the same in one piece."""
+    q, kv, cu, pos0, ks, vs = make(lens, past, H_q, H_kv, d, page, dtype, tail=2)
+    total = sum(lens)
+    pre = None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device=DEV)
+    n = gdn.gdn_attn_prefill_workspace_size(kv, len(lens), total + 2, H_q)
+    assert n > 256                                          # it would be split
+    opts = dict(prefix_len=pre, softcap=softcap, window=window)
+    first = None
+    for ws in (torch.zeros(n, dtype=torch.uint8, device=DEV), None,
+               torch.full((n - 1,), 0, dtype=torch.uint8, device=DEV)):
+        out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=DEV)
+        gdn.gdn_attn_prefill(q, kv, cu, pos0, out=out, lse=lse, workspace=ws, **opts)
+        if ws is not None:
+            assert gdn.gdn_get_device_error(ws) == gdn.GDN_OK
+        verify(out, lse, q, ks, vs, lens, past, d ** -0.5, softcap,
+               lambda i: seen_by(lens[i], past[i], window, prefix[i] if prefix else 0))
+        assert bool((out[total:] == 7.0).all()) and bool((lse[total:] == 7.0).all())
+        if first is None:
+            first = out
+        elif ws is None:
+            assert torch.equal(out, first)                  # split the same way, same order of sums
+
+
+def test_wide_table_short_context():
+    """A table that could hold a long context, and sequences that do not: nothing is split."""
+    q, kv, cu, pos0, ks, vs = make([70, 12], [30, 0], 8, 2, 128, 16, BF)
+    wide = torch.full((2, 4096), -1, dtype=torch.int32, device=DEV)
+    wide[:, :kv.page_table.shape[1]] = kv.page_table
+    big = gdn.PagedKV(kv.k, kv.v, wide)
+    assert gdn.gdn_attn_prefill_workspace_size(big, 2, 82, 8) > 256
+    out, lse = gdn.gdn_attn_prefill(q, big, cu, pos0)
+    verify(out, lse, q, ks, vs, [70, 12], [30, 0], 128 ** -0.5, 0.0,
+           lambda n: seen_by([70, 12][n], [30, 0][n]))
+    small, _ = gdn.gdn_attn_prefill(q, kv, cu, pos0)
+    assert torch.equal(small, out)
 
 
 def test_dense_batch_equals_packed():
