@@ -16,7 +16,7 @@
  * With p the position of a query, h its head and h' = h / (H_q / H_kv) its key head:
  *
  *     x_t = scale * q . k_t                 (k_t, v_t: key and value of token t, head h')
- *     x_t = softcap * tanh(x_t / softcap)   when softcap > 0
+ *     x_t = softcap * tanh(x_t / softcap)   unless softcap is 0 (else 1e-4 .. 1e6)
  *     out = sum_t exp(x_t) v_t / sum_t exp(x_t),   lse = ln sum_t exp(x_t)
  *
  * over the tokens t that the query sees (each call says which).  A query that sees none

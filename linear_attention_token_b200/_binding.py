@@ -592,11 +592,15 @@ def _token_rows(t, name, T_total, heads, kv):
     if t.is_contiguous():
         return t.data_ptr(), shape[-2] * d
     stride = t.stride()
-    if len(shape) == 4 and shape[0] > 1 and stride[0] != shape[1] * stride[1]:
-        raise ValueError(f"{name}'s tokens must be evenly spaced")
+    apart = stride[-3]
+    if len(shape) == 4 and shape[0] > 1:
+        if shape[1] == 1:
+            apart = stride[0]
+        elif stride[0] != shape[1] * apart:
+            raise ValueError(f"{name}'s tokens must be evenly spaced")
     if stride[-1] != 1 or (stride[-2] != d and shape[-2] > 1):
         raise ValueError(f"{name}'s heads and dims must be contiguous")
-    return t.data_ptr(), stride[-3]
+    return t.data_ptr(), apart
 
 
 def _sequences(x, cu_seqlens, kv):

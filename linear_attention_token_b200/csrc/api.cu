@@ -507,7 +507,8 @@ int sm_count()
     const int sms = gdn::device_sm_count();
     return sms > 0 ? sms : kDefaultSms;
 }
-bool softcap_ok(float cap) { return cap >= 0.f && cap < INFINITY; }
+// 0, or a cap that neither its quotient with the scale nor its score in base 2 can overflow
+bool softcap_ok(float cap) { return cap == 0.f || (cap >= 1e-4f && cap <= 1e6f); }
 bool scale_ok(float scale) { return scale > -INFINITY && scale < INFINITY; }
 }  // namespace
 

@@ -726,7 +726,8 @@ cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     }, &sms);
     if (e != cudaSuccess) return e;
-    const int grid = sms * kCtasPerSm;
+    // (fp32 rings of d = 128 leave room for one CTA an SM)
+    const int grid = sms * (2 * (smem + 1024) <= 233472 ? kCtasPerSm : 1);
     p.row_blocks = (p.rows + ROWS::kRows - 1) / ROWS::kRows;
     p.units_per_seq = p.cache.H_kv * p.row_blocks * (LIST ? p.T : 1);
     p.rec = static_cast<JoinRecord *>(workspace);

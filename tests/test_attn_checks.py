@@ -87,7 +87,8 @@ def decode(L, listed=False, **over):
 DECODE = PAGED + [
     (dict(T=0), UNSUPPORTED), (dict(T=9), UNSUPPORTED), (dict(H_q=3), BAD), (dict(H_q=0), BAD),
     (dict(H_q=8192), UNSUPPORTED), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
-    (dict(cap=-1.0), BAD), (dict(cap=float("nan")), BAD), (dict(q=None), BAD), (dict(q=A + 2), BAD),
+    (dict(cap=-1.0), BAD), (dict(cap=float("nan")), BAD), (dict(cap=1e-5), BAD), (dict(cap=1e7), BAD),
+    (dict(q=None), BAD), (dict(q=A + 2), BAD),
     (dict(q_pos=None), BAD), (dict(q_pos=A + 2), BAD), (dict(out=None), BAD), (dict(lse=A + 2), BAD),
     (dict(ws=None), BAD), (dict(ws=A + 8), BAD), (dict(ws_bytes=1024), BAD)]
 

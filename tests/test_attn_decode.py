@@ -166,6 +166,18 @@ def test_workspace_of_any_contents():
             assert torch.equal(o, out) and torch.equal(l, lse)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale,softcap", [(-0.1, 0.0), (0.0, 0.0), (2.0, 5.0), (-1.0, 1.0), (0.0, 3.0)])
+def test_scale_of_any_sign_and_far_caps(scale, softcap, dtype):
+    """Scores on both sides of the cap, where the cap's two forms meet."""
+    q, pos, kv, ks, vs = make([300, 20], 2, 4, 2, 64, 16, dtype)
+    out, lse = gdn.gdn_attn_decode(q, pos, kv, scale=scale, softcap=softcap)
+    verify(out, lse, q, ks, vs, lambda n, j: torch.arange([300, 20][n] - 1 + j, device=DEV), scale,
+           softcap, dtype)
+    again, none = gdn.gdn_attn_decode(q, pos, kv, scale=scale, softcap=softcap, want_lse=False)
+    assert none is None and torch.equal(again, out)
+
+
 def test_peaked_scores():
     """Scores of hundreds, of both signs: one key decides, and the running maximum jumps."""
     q, pos, kv, ks, vs = make([2000], 1, 8, 2, 128, 16, torch.bfloat16, by=60.0)
