@@ -3,12 +3,12 @@
 Every step of the gated delta rule runs in libgdn's CUDA kernels; this module
 passes torch device pointers, sizes and the current CUDA stream through the C ABI
 and turns status codes into exceptions.  There is no fallback: if libgdn.so is
-missing, or a tensor is not on a CUDA device, the call raises.
+missing, or a tensor is not on a CUDA device, the call raises.  The paged cache's calls, which
+take only microseconds, go through _marshal.so (csrc/marshal.cpp) instead of ctypes.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -506,8 +506,7 @@ class PagedKV:
     the library reads; their contents may change at any time, the tensors themselves may not
     (make another PagedKV for another table)."""
 
-    __slots__ = ("k", "v", "page_table", "dtype", "device", "index", "H_kv", "d", "seqs", "code",
-                 "ref", "_struct")
+    __slots__ = ("k", "v", "page_table", "dtype", "device", "H_kv", "d", "handle", "_struct")
 
     def __init__(self, k, v, page_table):
         code = _dtype_code(k)
@@ -527,102 +526,43 @@ class PagedKV:
             if t.device != k.device:
                 raise ValueError(f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.page_table = k, v, page_table
-        self.dtype, self.device, self.index, self.code = k.dtype, k.device, k.get_device(), code
+        self.dtype, self.device = k.dtype, k.device
         num_pages, page_size, self.H_kv, self.d = k.shape
-        self.seqs = page_table.shape[0]
+        self.handle = _marshal().cache(k, v, page_table)
         self._struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), num_pages,
                                       page_table.shape[1], page_size, self.H_kv, self.d, code)
-        self.ref = ctypes.byref(self._struct)
 
 
-def _launch_stream(kv) -> int:
-    """The current stream; every operand was found on the cache's device before."""
-    if kv.index < 0:
-        raise ValueError("the cache must be in CUDA tensors (libgdn has no CPU path)")
-    return torch._C._cuda_getCurrentRawStream(kv.index)
+_marshal_module = None
 
 
-def _placed(fn):
-    """Run `fn` on the device of its first tensor and, when `stream` is given, with that stream
-    current, so that what the call allocates belongs to the stream it is used on."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        index = first.get_device()
-        if index >= 0:
-            if stream is not None:
-                if stream.device.index != index:
-                    raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
-                with torch.cuda.stream(stream):
-                    return fn(first, *args, **kw)
-            if index != torch._C._cuda_getDevice():
-                with torch.cuda.device(index):
-                    return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-    return call
+def _marshal():
+    """The marshalling module (raises if it has not been built)."""
+    global _marshal_module
+    if _marshal_module is None:
+        lib()
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("_marshal.so could not be loaded; build it with "
+                               "`python -m linear_attention_token_b200.build`") from e
+        _marshal_module = module
+    return _marshal_module
 
 
-def _addr(t, name, dtype, shape, kv):
-    """Device address of an operand (None stays None) after checking type, shape, layout and
-    device.  (These checks run on every call of small kernels: one compare each.)"""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != kv.index:
-        raise ValueError(f"{name} is on {t.device}, the cache on {kv.device}")
-    return t.data_ptr()
-
-
-def _token_rows(t, name, T_total, heads, kv):
-    """Address and token stride of [T_total, heads, d] (or [B, T, heads, d]) whose heads and dims
-    are contiguous; tokens may lie further apart."""
-    shape, d = t.shape, kv.d
-    if t.dtype is not kv.dtype:
-        raise TypeError(f"{name} must have the cache's dtype {kv.dtype}, got {t.dtype}")
-    if t.get_device() != kv.index:
-        raise ValueError(f"{name} is on {t.device}, the cache on {kv.device}")
-    if len(shape) not in (3, 4) or shape[-1] != d or (heads is not None and shape[-2] != heads):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [.., {heads}, {d}]")
-    if t.numel() != T_total * shape[-2] * d:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {T_total} tokens")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-2] * d
-    stride = t.stride()
-    apart = stride[-3]
-    if len(shape) == 4 and shape[0] > 1:
-        if shape[1] == 1:
-            apart = stride[0]
-        elif stride[0] != shape[1] * apart:
-            raise ValueError(f"{name}'s tokens must be evenly spaced")
-    if stride[-1] != 1 or (stride[-2] != d and shape[-2] > 1):
-        raise ValueError(f"{name}'s heads and dims must be contiguous")
-    return t.data_ptr(), apart
-
-
-def _sequences(x, cu_seqlens, kv):
-    """(T_total, num_seqs) of packed [T_total, H, d] with offsets, or dense [B, T, H, d]."""
-    if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32:
-            raise TypeError("cu_seqlens must be int32")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
-        if x.dim() != 3:
-            raise ValueError("packed tokens must be [T_total, heads, d]")
-        T_total, N = x.shape[0], cu_seqlens.numel() - 1
-    elif x.dim() == 4:
-        N = x.shape[0]
-        T_total = N * x.shape[1]
-    elif x.dim() == 3:
-        N, T_total = 1, x.shape[0]
+def _run(where, call, kv, stream, args):
+    """`call` with the cache's device and, when given, `stream` current, so that what the call
+    allocates belongs to the stream it is used on; a status becomes a GdnError."""
+    if stream is None:
+        r = call(kv.handle, *args)
     else:
-        raise ValueError("tokens must be [T_total, heads, d] or [B, T, heads, d]")
-    if N > kv.seqs:
-        raise ValueError(f"page_table has {kv.seqs} rows for {N} sequences")
-    return T_total, N
+        if stream.device != kv.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {kv.device}")
+        with torch.cuda.stream(stream):
+            r = call(kv.handle, *args)
+    if r.__class__ is int:
+        raise GdnError(r, where)
+    return r
 
 
 def rope_inv_freq(rope_dims: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -631,9 +571,9 @@ def rope_inv_freq(rope_dims: int, base: float = 10000.0, device="cuda") -> torch
     return (float(base) ** (-i / rope_dims)).float().to(device)
 
 
-@_placed
 def gdn_kv_append(k, v, kv: PagedKV, cu_seqlens=None, pos0=None, *, q=None, q_out=None,
-                  inv_freq=None, rope_pos=None, rope_sections=None, interleaved: bool = False):
+                  inv_freq=None, rope_pos=None, rope_sections=None, interleaved: bool = False,
+                  stream=None):
     """Put a call's keys and values into the cache, the keys rotated on the way, and rotate its
     queries.  k, v [T_total, H_kv, d] with cu_seqlens int32 [N + 1], or [B, T, H_kv, d]; tokens
     may lie further apart than their heads (a slice of a fused projection).  pos0 int32 [N]:
@@ -641,39 +581,8 @@ def gdn_kv_append(k, v, kv: PagedKV, cu_seqlens=None, pos0=None, *, q=None, q_ou
     (None: no rotation); rope_pos int32 [n_axes, T_total] with rope_sections (a tuple of n_axes
     frequency counts) rotates at other positions than the cache's.  Returns q_out (q's shape,
     contiguous; it may be q itself), or None without q."""
-    T_total, N = _sequences(k, cu_seqlens, kv)
-    kp, ks = _token_rows(k, "k", T_total, kv.H_kv, kv)
-    vp, vs = _token_rows(v, "v", T_total, kv.H_kv, kv)
-    qp, qs, qo, H_q = None, 0, None, 0
-    if q is not None:
-        qp, qs = _token_rows(q, "q", T_total, None, kv)
-        H_q = q.shape[-2]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=kv.dtype, device=kv.device)
-        qo = _addr(q_out, "q_out", kv.dtype, q.shape, kv)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    rope_dims, n_axes, sections = 0, 1, None
-    if inv_freq is not None:
-        rope_dims = 2 * inv_freq.numel()
-        if rope_sections is not None:
-            n_axes = len(rope_sections)
-            if n_axes < 1 or n_axes > GDN_ROPE_MAX_AXES:
-                raise ValueError(f"rope_sections must have 1 to {GDN_ROPE_MAX_AXES} entries")
-            if n_axes > 1 and rope_pos is None:
-                raise ValueError("several axes need rope_pos")
-            sections = (ctypes.c_int32 * n_axes)(*rope_sections)
-    elif rope_pos is not None or rope_sections is not None:
-        raise ValueError("rope_pos and rope_sections need inv_freq")
-    st = lib().gdn_kv_append(
-        kv.ref, kp, vp, qp, qo, ks, vs, qs,
-        _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), kv),
-        _addr(pos0, "pos0", torch.int32, (N,), kv), N, T_total, H_q,
-        _addr(inv_freq, "inv_freq", torch.float32, (rope_dims // 2,), kv), rope_dims,
-        _addr(rope_pos, "rope_pos", torch.int32, (n_axes, T_total), kv), sections, n_axes,
-        GDN_ROPE_INTERLEAVED if interleaved else 0, _launch_stream(kv))
-    _check(st, "gdn_kv_append")
-    return q_out
+    return _run("gdn_kv_append", _marshal().append, kv, stream,
+                (k, v, cu_seqlens, pos0, q, q_out, inv_freq, rope_pos, rope_sections, interleaved))
 
 
 def gdn_attn_decode_workspace_size(n_queries: int, H_q: int, H_kv: int, d: int,
@@ -690,68 +599,33 @@ def attn_decode_workspace(n_queries: int, H_q: int, H_kv: int, d: int, dtype=tor
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_operands(q, q_pos, kv, out, lse, want_lse, workspace):
-    if q.dim() != 4 or q.shape[3] != kv.d:
-        raise ValueError(f"q must be [N, n_queries, H_q, {kv.d}], got {tuple(q.shape)}")
-    N, T, H_q = q.shape[:3]
-    dev = kv.device
-    if N > kv.seqs:
-        raise ValueError(f"page_table has {kv.seqs} rows for {N} sequences")
-    qp = _addr(q, "q", kv.dtype, q.shape, kv)
-    if out is None:
-        out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty(N, T, H_q, dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = attn_decode_workspace(T, H_q, kv.H_kv, kv.d, kv.dtype, dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    return (out, lse, N, T, H_q, qp, _addr(q_pos, "q_pos", torch.int32, (N,), kv),
-            _addr(out, "out", kv.dtype, q.shape, kv),
-            _addr(lse, "lse", torch.float32, (N, T, H_q), kv), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-
-
-@_placed
 def gdn_attn_decode(q, q_pos, kv: PagedKV, *, scale: Optional[float] = None, softcap: float = 0.0,
-                    window: int = 0, out=None, lse=None, want_lse: bool = True, workspace=None):
+                    window: int = 0, out=None, lse=None, want_lse: bool = True, workspace=None,
+                    stream=None):
     """Attention of the newest tokens over the whole cache: q [N, T, H_q, d] (query j of
     sequence n at position q_pos[n] + j, seeing the tokens at or before it, with window > 0 only
     the last `window` of them), q_pos int32 [N].  scale None is d^-0.5; softcap > 0 caps scores
     by a tanh.  Returns (out, lse [N, T, H_q] float32 or None)."""
-    out, lse, N, T, H_q, qp, pp, op, lp, wp, wn = _decode_operands(q, q_pos, kv, out, lse, want_lse,
-                                                                   workspace)
-    st = lib().gdn_attn_decode(qp, pp, kv.ref, op, lp, N, T, H_q,
-                               kv.d ** -0.5 if scale is None else scale, softcap, window, wp, wn,
-                               _launch_stream(kv))
-    _check(st, "gdn_attn_decode")
-    return out, lse
+    return _run("gdn_attn_decode", _marshal().decode, kv, stream,
+                (q, q_pos, None, 0, scale, softcap, window, out, lse, want_lse, workspace))
 
 
-@_placed
 def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
                         scale: Optional[float] = None, softcap: float = 0.0, out=None, lse=None,
-                        want_lse: bool = True, workspace=None):
+                        want_lse: bool = True, workspace=None, stream=None):
     """Attention of the newest tokens over listed tokens: as gdn_attn_decode, but query j of
     sequence n sees the tokens that token_idx[n, j] lists (int32 [N, T, L], or [N, L] for T = 1,
     as gdn_qsa_index_decode and gdn_qsa_index_multi return it; -1 pads) and the newest `recent`
     ones, each of those once.  Returns (out, lse)."""
-    out, lse, N, T, H_q, qp, pp, op, lp, wp, wn = _decode_operands(q, q_pos, kv, out, lse, want_lse,
-                                                                   workspace)
-    L = token_idx.shape[-1]
-    shape = (N, L) if T == 1 and token_idx.dim() == 2 else (N, T, L)
-    st = lib().gdn_qsa_attn_decode(qp, pp, kv.ref,
-                                   _addr(token_idx, "token_idx", torch.int32, shape, kv), L,
-                                   recent, op, lp, N, T, H_q,
-                                   kv.d ** -0.5 if scale is None else scale, softcap, wp, wn,
-                                   _launch_stream(kv))
-    _check(st, "gdn_qsa_attn_decode")
-    return out, lse
+    if token_idx is None:
+        raise ValueError("token_idx is required")
+    return _run("gdn_qsa_attn_decode", _marshal().decode, kv, stream,
+                (q, q_pos, token_idx, recent, scale, softcap, 0, out, lse, want_lse, workspace))
 
 
 def gdn_attn_prefill_workspace_size(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
                                     varlen: bool = True) -> int:
-    return int(lib().gdn_attn_prefill_workspace_size(kv.ref, int(varlen), num_seqs, T_total, H_q))
+    return int(lib().gdn_attn_prefill_workspace_size(ctypes.byref(kv._struct), int(varlen), num_seqs, T_total, H_q))
 
 
 def attn_prefill_workspace(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
@@ -764,10 +638,9 @@ def attn_prefill_workspace(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
     return workspace
 
 
-@_placed
 def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=None,
                      scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, out=None,
-                     lse=None, want_lse: bool = True, workspace=None):
+                     lse=None, want_lse: bool = True, workspace=None, stream=None):
     """Attention of prompts whose keys and values are in the cache already: q [T_total, H_q, d]
     with cu_seqlens int32 [N + 1], or [B, T, H_q, d]; query i of sequence n sits at position
     pos0[n] + i (pos0 None: 0) and sees the tokens at or before it, with window > 0 only the last
@@ -775,30 +648,5 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
     (attn_prefill_workspace; None takes one for the call) records a device-side timeout for
     gdn_get_device_error and lets few rows behind a long context use all SMs.  Returns (out, lse [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are
     left alone."""
-    T_total, N = _sequences(q, cu_seqlens, kv)
-    if q.shape[-1] != kv.d:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected head dim {kv.d}")
-    dev, H_q = kv.device, q.shape[-2]
-    qp = _addr(q, "q", kv.dtype, q.shape, kv)
-    if out is None:
-        out = torch.empty(q.shape, dtype=kv.dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    wp, wn = None, 0
-    if workspace is None and kv.index >= 0:
-        wn = lib().gdn_attn_prefill_workspace_size(kv.ref, cu_seqlens is not None, N, T_total, H_q)
-        if wn > 256:                              # 256: only the error word, which nobody would read
-            workspace = torch.empty(wn, dtype=torch.uint8, device=dev)
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}")
-        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = lib().gdn_attn_prefill(
-        qp, kv.ref, _addr(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), kv),
-        _addr(pos0, "pos0", torch.int32, (N,), kv),
-        _addr(prefix_len, "prefix_len", torch.int32, (N,), kv),
-        _addr(out, "out", kv.dtype, q.shape, kv),
-        _addr(lse, "lse", torch.float32, q.shape[:-1], kv), N, T_total, H_q,
-        kv.d ** -0.5 if scale is None else scale, softcap, window, wp, wn, _launch_stream(kv))
-    _check(st, "gdn_attn_prefill")
-    return out, lse
+    return _run("gdn_attn_prefill", _marshal().prefill, kv, stream,
+                (q, cu_seqlens, pos0, prefix_len, scale, softcap, window, out, lse, want_lse, workspace))

@@ -1,9 +1,10 @@
-"""Build libgdn.so in-tree with nvcc for sm_100a (no JIT, no torch extension).
+"""Build libgdn.so in-tree with nvcc for sm_100a (no JIT), and the binding's marshalling module.
 
     python -m linear_attention_token_b200.build [--force]
 
-The library is plain CUDA C++ behind the C ABI in include/gdn.h; Python reaches
-it through ctypes (linear_attention_token_b200/_binding.py).
+The library is plain CUDA C++ behind the C ABI in include/*.h; Python reaches it through
+ctypes (linear_attention_token_b200/_binding.py).  _marshal.so (csrc/marshal.cpp, g++ with
+torch's headers) checks the operands of the calls that take microseconds.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn.so")
+MARSHAL, MARSHAL_SRC = os.path.join(PKG, "_marshal.so"), os.path.join(CSRC, "marshal.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -40,14 +42,42 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """_marshal.so, linked to the libgdn.so beside it (built before)."""
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if not force and os.path.exists(MARSHAL) and all(
+            os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(ROOT, "include"), "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", MARSHAL + ".tmp",
+           "-L", PKG, "-l:libgdn.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale(LIB):
+        build_marshal(verbose=verbose)
         return LIB
     cmd = [NVCC, *NVCC_FLAGS, *extra, *sources(), "-o", LIB + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    build_marshal(force=force, verbose=verbose)
     return LIB
 
 

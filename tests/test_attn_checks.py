@@ -17,7 +17,7 @@ P = ctypes.c_void_p
 BAD, UNSUPPORTED = gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def L():
     gdn_build.build()
     return gdn.lib()
