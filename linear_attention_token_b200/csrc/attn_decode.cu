@@ -39,11 +39,11 @@ constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kLoadRows = 16;              // keys one warp loads per step
 
-// What CTA c leaves for the join: the unit that began in it and ends in a later CTA.
+// What the CTA in which a unit begins leaves for the join.
 struct JoinRecord {
     int n, sub;                            // sequence; unit within the sequence
-    int parts;                             // CTAs c .. c + parts - 1 hold a part (0: none)
-    int first_slot;                        // where CTA c's own part is (later ones: slot 0)
+    int parts;                             // CTAs c .. c + parts - 1 hold a part (0: nothing to join)
+    int place;                             // 2 c + where CTA c's own part is (later ones: slot 0)
 };
 
 struct DecodeParams {
@@ -54,7 +54,8 @@ struct DecodeParams {
     float *lse;
     float *part_o;                         // [grid, 2, rows, D]
     float2 *part_ml;                       // [grid, 2, rows]
-    JoinRecord *rec;                       // [grid]
+    JoinRecord *rec;                       // [grid]: by unit while there are no more than that, else by CTA
+    bool by_unit;
     int N, T, H_q, G;                      // G = H_q / H_kv
     int rows, row_blocks;                  // query rows of a unit (before blocking), blocks
     int units_per_seq;
@@ -516,7 +517,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     pdl_trigger();
     // all steps, and where this CTA's stretch begins
     const int cta = blockIdx.x;
-    if (tid == 0) p.rec[cta].parts = 0;
+    if (tid == 0 && !p.by_unit) p.rec[cta].parts = 0;
     long long W, begin, end;
     int G, n, sub, step;
     Span sp;
@@ -632,13 +633,13 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
                 if (c == 0) p.part_ml[pr] = make_float2(s.m, s.l);
             }
         }
-        if (step == 0 && !whole && tid == 0) {
+        if (step == 0 && tid == 0 && (p.by_unit || !whole)) {
             JoinRecord r;
             r.n = n;
             r.sub = sub;
-            r.parts = cta_of(W, G, at + sp.steps - 1) - cta + 1;
-            r.first_slot = slot;
-            p.rec[cta] = r;
+            r.parts = whole ? 0 : cta_of(W, G, at + sp.steps - 1) - cta + 1;
+            r.place = 2 * cta + slot;
+            p.rec[p.by_unit ? n * p.units_per_seq + sub : cta] = r;
         }
         at += count;
         step = 0;
@@ -658,29 +659,30 @@ template <> __device__ __forceinline__ void store2<__nv_bfloat16>(void *p, size_
     *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p) + i) = pack2(a, b);
 }
 
-// Joins the parts of the units that more than one CTA ran: CTA (c, r) of this grid joins row r
-// of the unit that began in CTA c, its warps taking the parts in turn.
+// Joins the parts of the units that more than one CTA ran, a record per blockIdx.x.  With few units
+// (many parts each) a CTA takes row blockIdx.y, its warps taking the parts in turn; with many (one or
+// two parts each) a warp takes a row, which keeps the grid small.
 constexpr int kJoinWarps = 8;
 
-template <typename E, int D, int ROWS, bool LIST>
+template <typename E, int D, int ROWS, bool LIST, bool FEW>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ DecodeParams p) {
-    __shared__ float so[kJoinWarps][D];
+    __shared__ float so[FEW ? kJoinWarps : 1][D];
     __shared__ float2 sml[kJoinWarps];
-    const int c = blockIdx.x, r = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int V = D / 32;
+    const int r = FEW ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
+    constexpr int V = D / 32, STEP = FEW ? kJoinWarps : 1;
     pdl_wait();
-    const JoinRecord rec = p.rec[c];
+    const JoinRecord rec = p.rec[blockIdx.x];
     if (rec.parts < 2) return;
     const Unit u = unit_of<LIST>(p, rec.n, rec.sub);
     const int row = u.rb * ROWS + r;
-    if (row >= p.rows) return;
+    if (r >= ROWS || row >= p.rows) return;
     float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < rec.parts; i += kJoinWarps) {
-        const size_t at = ((size_t)(c + i) * 2 + (i == 0 ? rec.first_slot : 0)) * ROWS + r;
+    for (int i = FEW ? warp : 0; i < rec.parts; i += STEP) {
+        const size_t at = (size_t)(i == 0 ? rec.place : (rec.place | 1) - 1 + 2 * i) * ROWS + r;
         const float2 ml = p.part_ml[at];
         const float *src = p.part_o + at * D + lane * V;
         const float mx = fmaxf(m, ml.x), shift = mx == -INFINITY ? 0.f : mx;
@@ -690,9 +692,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
         for (int e = 0; e < V; ++e) o[e] = o[e] * f + src[e] * g;
         m = mx;
     }
+    const size_t rh = row_head<LIST>(p, u, row);
+    if (!FEW) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) store2<E>(p.out, rh * D + lane * V + e, o[e] * inv, o[e + 1] * inv);
+        if (lane == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        return;
+    }
     if (lane == 0) sml[warp] = make_float2(m, l);
 #pragma unroll
-    for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+    for (int e = 0; e < V; ++e) so[FEW ? warp : 0][lane * V + e] = o[e];
     __syncthreads();
     if (threadIdx.x >= D / 2) return;
     m = -INFINITY;
@@ -706,10 +716,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     for (int w = 0; w < kJoinWarps; ++w) {
         const float f = ex2(sml[w].x - shift);
         l = fmaf(sml[w].y, f, l);
-        a = fmaf(so[w][col], f, a);
-        b = fmaf(so[w][col + 1], f, b);
+        a = fmaf(so[FEW ? w : 0][col], f, a);
+        b = fmaf(so[FEW ? w : 0][col + 1], f, b);
     }
-    const size_t rh = row_head<LIST>(p, u, row);
     const float inv = l > 0.f ? 1.f / l : 0.f;
     store2<E>(p.out, rh * D + col, a * inv, b * inv);
     if (threadIdx.x == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
@@ -730,21 +739,28 @@ cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
     const int grid = sms * (2 * (smem + 1024) <= 233472 ? kCtasPerSm : 1);
     p.row_blocks = (p.rows + ROWS::kRows - 1) / ROWS::kRows;
     p.units_per_seq = p.cache.H_kv * p.row_blocks * (LIST ? p.T : 1);
+    const long long units = (long long)p.N * p.units_per_seq;
+    p.by_unit = units <= grid;
     p.rec = static_cast<JoinRecord *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.rec + grid);
     p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)grid * 2 * ROWS::kRows);
     attn_decode_kernel<ROWS, D, LIST><<<grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rows = p.rows < ROWS::kRows ? p.rows : ROWS::kRows;
+    // (4 sequences x 2 heads of 1024 tokens: a CTA for each of 296 CTAs and 8 rows 12.3 us a call, for
+    // each unit and row 10.5)
+    const bool few = units * kJoinWarps < grid;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, p.rows < ROWS::kRows ? p.rows : ROWS::kRows);
+    cfg.gridDim = dim3(p.by_unit ? (unsigned)units : grid, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<typename ROWS::E, D, ROWS::kRows, LIST>, p);
+    return few ? cudaLaunchKernelEx(&cfg, attn_join_kernel<typename ROWS::E, D, ROWS::kRows, LIST, true>, p)
+               : cudaLaunchKernelEx(&cfg, attn_join_kernel<typename ROWS::E, D, ROWS::kRows, LIST, false>, p);
 }
 
 template <int D, bool LIST>
