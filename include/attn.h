@@ -103,7 +103,9 @@ size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, int32_t H_
  *   q, out   : [num_seqs, n_queries, H_q, d], 1 <= n_queries <= GDN_ATTN_MAX_QUERIES
  *   q_pos    : DEVICE int32 [num_seqs]; negative for an idle slot (its queries see nothing)
  *   lse      : [num_seqs, n_queries, H_q] fp32 or NULL
- * The tokens' keys and values, the queries' own among them, are in the cache already. */
+ * The tokens' keys and values, the queries' own among them, are in the cache already.
+ * (Many drafted tokens of wide groups run on gdn_attn_prefill's bf16 kernel, with its bounded
+ * waits: a workspace whose first 16 bytes are zero records a timeout for gdn_get_device_error.) */
 gdn_status gdn_attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *kv,
                            void *out, float *lse, int32_t num_seqs, int32_t n_queries,
                            int32_t H_q, float scale, float softcap, int32_t window,

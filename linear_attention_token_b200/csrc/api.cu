@@ -62,7 +62,8 @@ size_t attn_decode_workspace_bytes(int rows, int d, int sms);
 cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int32_t *q_pos,
                                const int32_t *list, int list_len, int recent, bool lists,
                                void *out, float *lse, int N, int T, int H_q, float scale,
-                               float cap, int window, void *workspace, cudaStream_t stream);
+                               float cap, int window, void *workspace, size_t workspace_bytes,
+                               int sms, uint32_t budget, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
                                 const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
                                 int N, long long T_total, int H_q, float scale, float cap, int window,
@@ -594,7 +595,8 @@ gdn_status attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *
         return GDN_ERR_INVALID_ARG;
     const cudaError_t e =
         gdn::launch_attn_decode(*kv, q, q_pos, list, list_len, recent, lists, out, lse, num_seqs,
-                                n_queries, H_q, scale, softcap, window, workspace, stream);
+                                n_queries, H_q, scale, softcap, window, workspace, workspace_bytes,
+                                sm_count(), g_wait_budget.load(), stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 }  // namespace

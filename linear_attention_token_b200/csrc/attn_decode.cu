@@ -34,10 +34,12 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStep = 64;                  // keys per step of a CTA, 16 per warp
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
-constexpr int kLoadRows = 16;              // keys one warp loads per step
+constexpr int kLoad = 16;                  // keys one warp loads per step
+constexpr int kStep = kWarps * kLoad;      // keys per step of a CTA
+constexpr float kLazy = 8.f;               // growth of a row's maximum (base 2) that its sums may lag:
+                                           // until then the old one serves, and nothing is rescaled
 
 // What the CTA in which a unit begins leaves for the join.
 struct JoinRecord {
@@ -123,12 +125,12 @@ __device__ __forceinline__ size_t row_head(const DecodeParams &p, const Unit &u,
 }
 
 // ------------------------------------------------------------------------------- loading
-// Token of key `key` (0..15) of warp `sub`'s share of a step, or -1: not seen by any query of the
+// Token of key `key` of warp `sub`'s share of a step, or -1: not seen by any query of the
 // unit.  (What nobody sees is not read: it may hold anything.)
 template <bool LIST>
 __device__ __forceinline__ int token_at(const DecodeParams &p, const Unit &u, const Span &sp,
                                         long long pos, int step, int sub, int key) {
-    const int i = step * kStep + sub * kLoadRows + key;
+    const int i = step * kStep + sub * kLoad + key;
     if (LIST) {
         const int list_pad = (p.list_len + kStep - 1) / kStep * kStep;
         const long long at = pos + u.j;
@@ -145,13 +147,13 @@ __device__ __forceinline__ int token_at(const DecodeParams &p, const Unit &u, co
     return seen ? (int)t : -1;
 }
 
-// One warp's 16 keys of one step into its 16 rows of a stage (rows of D elements, 16-byte
-// chunk c of row r at c ^ (r & 7)), keys at kdst, values at vdst.  Lane l < 16 holds the cache row
-// of key l; absent keys (-1) are zero-filled, so nothing a dead row holds reaches a product.
+// One warp's keys of one step into its rows of a stage (rows of D elements, 16-byte
+// chunk c of row r at c ^ (r & 7)), keys at kdst, values at vdst.  Lane l < 16 holds the cache
+// row of key l; absent keys (-1) are zero-filled, so nothing a dead row holds reaches a product.
 template <typename E, int D>
 __device__ __forceinline__ void load_keys(const DecodeParams &p, int h, int row, uint32_t kdst,
                                           uint32_t vdst) {
-    constexpr int CH = D * (int)sizeof(E) / 16, RPI = 32 / CH, ITER = kLoadRows / RPI;
+    constexpr int CH = D * (int)sizeof(E) / 16, RPI = 32 / CH, ITER = kLoad / RPI;
     const int lane = threadIdx.x & 31, c = lane % CH;
     const size_t pitch = (size_t)p.cache.H_kv * D * sizeof(E);
     const size_t off = (size_t)h * D * sizeof(E) + (size_t)c * 16;
@@ -188,7 +190,7 @@ template <int D, int TEAM, bool LIST>
 struct TensorRows {
     using E = __nv_bfloat16;
     static constexpr int kTeam = TEAM, kRows = 16 * TEAM;        // rows of a unit's block
-    static constexpr int kTileKeys = 16 * TEAM;
+    static constexpr int kTileKeys = kLoad * TEAM;
     uint32_t q[D / 16][4];
     float o[D / 8][4];
     float m[2], l[2];
@@ -253,19 +255,20 @@ struct TensorRows {
                 s[i][e] = live ? s[i][e] : -INFINITY;
                 mx[e >> 1] = fmaxf(mx[e >> 1], s[i][e]);
             }
-        float shift[2];
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            mx[e] = fmaxf(mx[e], m[e]);
-            shift[e] = mx[e] == -INFINITY ? 0.f : mx[e];
-            const float f = ex2(m[e] - shift[e]);               // 0 while m is -inf
-            m[e] = mx[e];
-            l[e] *= f;
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                mx[e] = fmaxf(mx[e], m[e]);
+                const float f = mx[e] == -INFINITY ? 1.f : ex2(m[e] - mx[e]);       // 0 while m is -inf
+                m[e] = mx[e];
+                l[e] *= f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) { o[i][2 * e] *= f; o[i][2 * e + 1] *= f; }
+                for (int i = 0; i < D / 8; ++i) { o[i][2 * e] *= f; o[i][2 * e + 1] *= f; }
+            }
         }
+        const float shift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         // rounded to bf16 for the product (each weight is off by half a step, 2^-8 of itself, at
         // most; over many keys the errors average out below the output's own rounding); the sum
         // takes the unrounded weights, so lse is exact to fp32
@@ -312,32 +315,33 @@ struct TensorRows {
 };
 
 // --------------------------------------------------------------------- fp32: CUDA cores
-// A warp's 16 keys against R query rows held in shared memory.  Scores: lane pair (key, half of
-// the dims); weights go through shared memory; outputs: lane owns D / 32 dims of every row.
+// A warp's keys against R query rows held in shared memory.  Scores: kLanes lanes a key, each some of
+// the dims; weights go through shared memory; outputs: lane owns D / 32 dims of every row.
 template <int D, int R, bool LIST>
 struct FmaRows {
     using E = float;
-    static constexpr int kTeam = 1, kRows = R, kTileKeys = 16, kV = D / 32;
-    float o[R][kV];
+    static constexpr int kTeam = 1, kRows = R, kTileKeys = kLoad, kV = D / 32;
+    static constexpr int kLanes = 32 / kLoad;                  // lanes that share a key
+    float2 o[R][kV / 2];
     float m[R], l[R];
-    long long pos0;
-    int row0;
+    int first[R], last[R];                 // tokens a row may see (dense)
 
-    // shared: q [R][D], then per warp weights [R][16]
+    // shared: q [R][D], then per warp weights [R][kLoad]
     __device__ void begin(const DecodeParams &p, const Unit &u, long long pos, float *shared) {
         for (int i = threadIdx.x; i < R * D; i += kThreads) {
             const int r = u.rb * R + i / D;
             shared[i] = r < p.rows ? __ldg(static_cast<const float *>(p.q) +
                                            row_head<LIST>(p, u, r) * D + i % D) : 0.f;
         }
-        pos0 = pos;
-        row0 = u.rb * R;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            const long long at = pos + (LIST ? 0 : (u.rb * R + r) / p.G);
+            last[r] = LIST ? INT32_MAX : (int)min(at, (long long)INT32_MAX);
+            first[r] = LIST || p.window <= 0 ? INT32_MIN : (int)max(at - p.window + 1, (long long)INT32_MIN);
             m[r] = -INFINITY;
             l[r] = 0.f;
 #pragma unroll
-            for (int e = 0; e < kV; ++e) o[r][e] = 0.f;
+            for (int e = 0; e < kV / 2; ++e) o[r][e] = make_float2(0.f, 0.f);
         }
         __syncthreads();
     }
@@ -345,13 +349,13 @@ struct FmaRows {
     __device__ __forceinline__ void tile(const DecodeParams &p, uint32_t kt, uint32_t vt,
                                          uint64_t present, long long token0, float *shared) {
         constexpr int CH = D / 4;
-        const int lane = threadIdx.x & 31, key = lane >> 1, half = lane & 1;
-        float s[R];
+        const int lane = threadIdx.x & 31, key = lane / kLanes, part = lane % kLanes;
+        float2 s2[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = 0.f;
+        for (int r = 0; r < R; ++r) s2[r] = make_float2(0.f, 0.f);
 #pragma unroll 4
-        for (int c = 0; c < CH / 2; ++c) {
-            const int ch = 2 * c + half;                        // the pair reads neighbours
+        for (int c = 0; c < CH / kLanes; ++c) {
+            const int ch = kLanes * c + part;                   // a key's lanes read neighbours
             float4 k;
             asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                          : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
@@ -359,50 +363,73 @@ struct FmaRows {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float4 q = *reinterpret_cast<const float4 *>(shared + r * D + ch * 4);
-                s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                s2[r] = fma2(make_float2(q.x, q.y), make_float2(k.x, k.y), s2[r]);
+                s2[r] = fma2(make_float2(q.z, q.w), make_float2(k.z, k.w), s2[r]);
             }
         }
-        float *w = shared + R * D + (threadIdx.x >> 5) * R * 16;
-        const long long t = token0 + key;
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
-        score2(s, p.score);
+        float *w = shared + R * D + (threadIdx.x >> 5) * R * kLoad;
+        float s[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            bool live = (present >> key) & 1;
-            if (!LIST) {
-                const long long at = pos0 + (row0 + r) / p.G;
-                live = live && t <= at && (p.window <= 0 || t > at - p.window);
-            }
-            const float x = live ? s[r] : -INFINITY;
-            float mx = x;
+            s[r] = s2[r].x + s2[r].y;
 #pragma unroll
-            for (int d = 2; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            mx = fmaxf(mx, m[r]);
-            const float shift = mx == -INFINITY ? 0.f : mx;
-            const float f = ex2(m[r] - shift), e = ex2(x - shift);
-            m[r] = mx;
-            l[r] = l[r] * f + (half ? 0.f : e);
-#pragma unroll
-            for (int v = 0; v < kV; ++v) o[r][v] *= f;
-            if (half == 0) w[r * 16 + key] = e;
+            for (int d = 1; d < kLanes; d <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], d);
         }
-        __syncwarp();
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-            float v[kV];
-            const uint32_t at = vt + (uint32_t)(k * CH + ((lane * kV >> 2) ^ (k & 7))) * 16;
-            if constexpr (kV == 4)
-                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                             : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at) : "memory");
-            else
-                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
-                             : "=f"(v[0]), "=f"(v[1]) : "r"(at + (lane & 1) * 8) : "memory");
+        score2(s, p.score);
+        const int t = (int)(token0 + key);
+        const bool there = (present >> key) & 1;
+        bool grow = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!there || (!LIST && (t > last[r] || t < first[r]))) s[r] = -INFINITY;
+            grow = grow || s[r] > m[r] + kLazy;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float x = w[r * 16 + k];
+                float mx = s[r];
 #pragma unroll
-                for (int e = 0; e < kV; ++e) o[r][e] = fmaf(x, v[e], o[r][e]);
+                for (int d = kLanes; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                mx = fmaxf(mx, m[r]);
+                const float f = mx == -INFINITY ? 1.f : ex2(m[r] - mx);             // 0 while m is -inf
+                m[r] = mx;
+                l[r] *= f;
+#pragma unroll
+                for (int v = 0; v < kV / 2; ++v) o[r][v] = make_float2(o[r][v].x * f, o[r][v].y * f);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float e = ex2(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+            if (part == 0) {
+                l[r] += e;
+                w[r * kLoad + key] = e;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k0 = 0; k0 < kLoad; k0 += 4) {
+            float2 v[4][kV / 2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t at = vt + (uint32_t)((k0 + k) * CH + ((lane * kV >> 2) ^ ((k0 + k) & 7))) * 16;
+                if constexpr (kV == 4)
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(v[k][0].x), "=f"(v[k][0].y), "=f"(v[k][1].x), "=f"(v[k][1].y) : "r"(at) : "memory");
+                else
+                    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                                 : "=f"(v[k][0].x), "=f"(v[k][0].y) : "r"(at + (lane & 1) * 8) : "memory");
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 x = *reinterpret_cast<const float4 *>(w + r * kLoad + k0);
+#pragma unroll
+                for (int e = 0; e < kV / 2; ++e) {
+                    o[r][e] = fma2(make_float2(x.x, x.x), v[0][e], o[r][e]);
+                    o[r][e] = fma2(make_float2(x.y, x.y), v[1][e], o[r][e]);
+                    o[r][e] = fma2(make_float2(x.z, x.z), v[2][e], o[r][e]);
+                    o[r][e] = fma2(make_float2(x.w, x.w), v[3][e], o[r][e]);
+                }
             }
         }
         __syncwarp();
@@ -415,7 +442,8 @@ struct FmaRows {
             const float sum = warp_sum(l[r]);
             if (lane == 0) sml[r] = make_float2(m[r], sum);
 #pragma unroll
-            for (int e = 0; e < kV; ++e) so[r * D + lane * kV + e] = o[r][e];
+            for (int e = 0; e < kV / 2; ++e)
+                *reinterpret_cast<float2 *>(so + r * D + lane * kV + 2 * e) = o[r][e];
         }
     }
 };
@@ -429,7 +457,7 @@ struct Layout {
     static constexpr int kRing = kStages * 2 * kStageBytes;
     // the join of the CTA's teams reuses the ring
     static constexpr int kJoin = kTeams * ROWS::kRows * (D + 2) * 4;
-    static constexpr int kExtra = sizeof(typename ROWS::E) == 4 ? (ROWS::kRows * D + kWarps * ROWS::kRows * 16) * 4 : 0;
+    static constexpr int kExtra = sizeof(typename ROWS::E) == 4 ? (ROWS::kRows * D + kWarps * ROWS::kRows * kLoad) * 4 : 0;
     static constexpr int kMask = kStages * kWarps * 4;
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
     static constexpr int kSmem = kBody + kExtra + kMask + 64;
@@ -579,7 +607,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         // tokens are looked up two steps, cache rows one step before their loads go out, so that
         // the chain list -> page table -> key never stalls a step
         auto token = [&](int i) {
-            return i < count ? token_at<LIST>(p, u, sp, pos, step + i, warp, lane & 15) : -1;
+            return i < count ? token_at<LIST>(p, u, sp, pos, step + i, warp, lane % kLoad) : -1;
         };
         int row = cache_row(p.cache, n, token(0)), t_ahead = token(1);
         auto load = [&](int i) {
@@ -587,9 +615,9 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
             t_ahead = token(i + 2);
             if (i < count) {
                 const int st = i % kStages;
-                const uint32_t dst = ring + st * 2 * L::kStageBytes + warp * kLoadRows * L::kRowBytes;
+                const uint32_t dst = ring + st * 2 * L::kStageBytes + warp * kLoad * L::kRowBytes;
                 load_keys<E, D>(p, u.h, row, dst, dst + L::kStageBytes);
-                const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+                const uint32_t present = __ballot_sync(0xffffffffu, row >= 0) & ((1u << kLoad) - 1);
                 if (lane == 0) masks[st * kWarps + warp] = present;
             }
             cp_commit();
@@ -777,19 +805,42 @@ cudaError_t launch_dim(const DecodeParams &p, bool bf16, void *ws, cudaStream_t 
 
 constexpr int kMostRows = 64;              // largest ROWS::kRows
 
+// Whether a call's drafted tokens make enough rows for the prompt kernel (attn_prefill.cu), whose
+// tcgen05 products take 128 rows at the pace of one.  With more than 32 rows to a block of it, mma.sync
+// row tiles no longer keep up with the cache (64 sequences x 2 heads x 4096 tokens, 64 rows: 91
+// against 60 us, 128 rows: 162 against 60; 32 rows: 60 both); with fewer than 8 units the even split
+// over all SMs wins all the same (1 sequence x 2 heads x 8000 tokens, 64 rows: 19 against 24 us).
+bool many_rows(int N, int T, int H_kv, int G) {
+    int pack = 1;
+    while (pack < 16 && G % (2 * pack) == 0) pack *= 2;
+    return T * pack > 32 && (long long)N * H_kv >= 8;
+}
+
 }  // namespace
+
+cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
+                                const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
+                                int N, long long T_total, int H_q, float scale, float cap, int window,
+                                void *workspace, size_t workspace_bytes, int sms, uint32_t budget,
+                                cudaStream_t stream);
 
 // `rows`: query rows that share a key head (H_q / H_kv x n_queries), blocked as launch_dim does
 size_t attn_decode_workspace_bytes(int rows, int d, int sms) {
     const size_t block = rows <= 16 ? 16 : rows <= 32 ? 32 : kMostRows;
-    return (size_t)sms * kCtasPerSm *
-           (sizeof(JoinRecord) + 2 * block * (sizeof(float2) + d * sizeof(float)));
+    const size_t own = (size_t)sms * kCtasPerSm *
+                       (sizeof(JoinRecord) + 2 * block * (sizeof(float2) + d * sizeof(float)));
+    // (a call that the prompt kernel takes needs a little more for its table of blocks)
+    return rows > 32 ? own + ((size_t)64 << 10) : own;
 }
 
 cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int32_t *q_pos,
                                const int32_t *list, int list_len, int recent, bool lists,
                                void *out, float *lse, int N, int T, int H_q, float scale,
-                               float cap, int window, void *workspace, cudaStream_t stream) {
+                               float cap, int window, void *workspace, size_t workspace_bytes,
+                               int sms, uint32_t budget, cudaStream_t stream) {
+    if (!lists && kv.dtype == GDN_BF16 && many_rows(N, T, kv.H_kv, H_q / kv.H_kv))
+        return launch_attn_prefill(kv, q, nullptr, q_pos, nullptr, out, lse, N, (long long)N * T, H_q,
+                                   scale, cap, window, workspace, workspace_bytes, sms, budget, stream);
     DecodeParams p = {};
     p.cache = paged_view(kv);
     p.q = q;

@@ -49,30 +49,6 @@ constexpr int kTile = kPrefillTile;        // query rows of a tile, tokens of a 
 constexpr uint32_t kPollNs = 2000, kDrainBudget = GDN_DEFAULT_WAIT_BUDGET;
 constexpr float kLazy = 8.f;               // growth of a row maximum (base 2) that O may lag
 
-// Two fp32 lanes per instruction, and the larger of three.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 // cap2 tanh(y) + add, by the polynomial of degree DEG
 template <int DEG>
 __device__ __forceinline__ float2 capped_near_add2(float2 y, float cap2, float2 add) {
@@ -83,6 +59,7 @@ __device__ __forceinline__ float2 capped_near_add2(float2 y, float cap2, float2 
         r = fma2(r, t, make_float2(tanh_r<DEG>(i) * cap2, tanh_r<DEG>(i) * cap2));
     return fma2(y, r, add);
 }
+// the larger of three
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

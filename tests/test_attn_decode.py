@@ -56,6 +56,9 @@ CASES = [
     ([700, 260, 5], 2, 8, 2, 128, 16, 0.0, 100, torch.bfloat16),
     ([700, 260, 5], 4, 8, 2, 128, 16, 30.0, 1, torch.bfloat16),
     ([5000], 1, 6, 3, 128, 1024, 0.0, 0, torch.bfloat16),
+    ([500, 9, 130, 0, 1500], 4, 32, 2, 128, 16, 0.0, 0, torch.bfloat16),   # 64 rows, 10 units
+    ([700, 40, 300, 5], 8, 16, 2, 64, 64, 20.0, 0, torch.bfloat16),
+    ([4000] + [30] * 9, 3, 16, 1, 128, 16, 0.0, 900, torch.bfloat16),
     ([1, 2, 15, 16, 17, 0], 1, 4, 2, 128, 16, 0.0, 0, torch.float32),
     ([63, 1000], 1, 2, 2, 64, 16, 0.0, 0, torch.float32),
     ([500, 3, 77], 3, 8, 2, 64, 32, 15.0, 0, torch.float32),          # 12 rows: two blocks
