@@ -705,20 +705,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
     const Unit u = unit_of<LIST>(p, rec.n, rec.sub);
     const int row = u.rb * ROWS + r;
     if (r >= ROWS || row >= p.rows) return;
+    // this warp's parts: first, first + STEP, ..; a lane weighs one, and their outputs, which do not
+    // wait for the weights, come in several at a time
+    const int first = FEW ? warp : 0, count = rec.parts > first ? (rec.parts - first + STEP - 1) / STEP : 0;
+    auto place = [&](int k) -> size_t {
+        const int i = first + k * STEP;
+        return (size_t)(i == 0 ? rec.place : (rec.place | 1) - 1 + 2 * i) * ROWS + r;
+    };
     float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int i = FEW ? warp : 0; i < rec.parts; i += STEP) {
-        const size_t at = (size_t)(i == 0 ? rec.place : (rec.place | 1) - 1 + 2 * i) * ROWS + r;
-        const float2 ml = p.part_ml[at];
-        const float *src = p.part_o + at * D + lane * V;
-        const float mx = fmaxf(m, ml.x), shift = mx == -INFINITY ? 0.f : mx;
-        const float f = ex2(m - shift), g = ex2(ml.x - shift);
-        l = l * f + ml.y * g;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        const float2 ml = k0 + lane < count ? p.part_ml[place(k0 + lane)] : make_float2(-INFINITY, 0.f);
+        float mx = fmaxf(m, ml.x);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = o[e] * f + src[e] * g;
+        for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float shift = mx == -INFINITY ? 0.f : mx, old = ex2(m - shift), f = ex2(ml.x - shift);
         m = mx;
+        l = l * old + warp_sum(ml.y * f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= old;
+        const int n = min(32, count - k0);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float g = __shfl_sync(0xffffffffu, f, k);
+            const float *src = p.part_o + place(k0 + k) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(src);
+                o[0] = fmaf(x.x, g, o[0]);
+                o[1] = fmaf(x.y, g, o[1]);
+                o[2] = fmaf(x.z, g, o[2]);
+                o[3] = fmaf(x.w, g, o[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(src);
+                o[0] = fmaf(x.x, g, o[0]);
+                o[1] = fmaf(x.y, g, o[1]);
+            }
+        }
     }
     const size_t rh = row_head<LIST>(p, u, row);
     if (!FEW) {

@@ -22,8 +22,10 @@ cudaError_t launch_attn_prefill_f32(const AttnPrefillParams &p, int d, cudaStrea
 
 namespace {
 
+constexpr int kMaxSplits = 64;
+
 // Row r of block (x, r) from its parts: out = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i.  A warp
-// takes a row.  A part without tokens (l = 0) has no outputs and is not read.
+// takes a row.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_constant__ AttnPrefillParams p,
                                                                 int rows) {
@@ -34,21 +36,38 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
     const int token = (b.row0 + r) / max(b.pack, 1);
     if (b.parts < 2 || token >= b.len) return;
     const size_t at0 = (size_t)blockIdx.x * p.splits * rows + r;
-    float m = -INFINITY;
-    for (int i = 0; i < b.parts; ++i) m = fmaxf(m, p.part_ml[at0 + (size_t)i * rows].x);
+    // a lane weighs a part (or two: there are at most kMaxSplits), and the outputs, which do not wait for
+    // the weights, come in several at a time
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 ml0 = lane < b.parts ? p.part_ml[at0 + (size_t)lane * rows] : none;
+    const float2 ml1 = lane + 32 < b.parts ? p.part_ml[at0 + (size_t)(lane + 32) * rows] : none;
+    float m = fmaxf(ml0.x, ml1.x);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float shift = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
+    // a part without tokens (l = 0) wrote no outputs: it is not read
+    const float f0 = ml0.y > 0.f ? ex2(ml0.x - shift) : 0.f, f1 = ml1.y > 0.f ? ex2(ml1.x - shift) : 0.f;
+    const float l = warp_sum(ml0.y * f0 + ml1.y * f1);
+    const uint32_t some[2] = {__ballot_sync(0xffffffffu, ml0.y > 0.f), __ballot_sync(0xffffffffu, ml1.y > 0.f)};
+    float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < b.parts; ++i) {
-        const size_t at = at0 + (size_t)i * rows;
-        const float2 ml = p.part_ml[at];
-        if (ml.y == 0.f) continue;
-        const float f = ex2(ml.x - shift);
-        l = fmaf(ml.y, f, l);
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(p.part_o[at * D + lane * V + e], f, o[e]);
+        if (!((some[i >> 5] >> (i & 31)) & 1)) continue;
+        const float f = __shfl_sync(0xffffffffu, i < 32 ? f0 : f1, i & 31);
+        const float *src = p.part_o + (at0 + (size_t)i * rows) * D + lane * V;
+        if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(src);
+            o[0] = fmaf(x.x, f, o[0]);
+            o[1] = fmaf(x.y, f, o[1]);
+            o[2] = fmaf(x.z, f, o[2]);
+            o[3] = fmaf(x.w, f, o[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(src);
+            o[0] = fmaf(x.x, f, o[0]);
+            o[1] = fmaf(x.y, f, o[1]);
+        }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const size_t rh = (size_t)(b.first + token) * p.H_q + b.h0 + (b.row0 + r) % b.pack;
@@ -64,7 +83,6 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
 }
 
 constexpr size_t kErrorBytes = 256;        // the error word, padded
-constexpr int kMaxSplits = 64;
 
 struct Shape {
     int pack_shift, rows, splits;          // heads packed into a row tile (bf16), rows of a block
