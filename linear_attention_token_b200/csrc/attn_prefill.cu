@@ -468,6 +468,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     commit(B_DRAIN);
                     mbar_wait(bars + B_DRAIN, 0, kDrainBudget);
                 }
+            } else {
+                // so they do here, also when the softmax warps give up on the last ones
+                if (tiles_a > 0) mbar_wait(bars + B_O, 0, kDrainBudget);
+                if (tiles_b > 0) mbar_wait(bars + B_O + 1, 0, kDrainBudget);
             }
             __syncwarp();
         } else if (warp == 10) {
@@ -499,6 +503,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     reinterpret_cast<uint32_t *>(sm + L::kMask + (j % kMaskRing) * 16)[lane] =
                         (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
                 }
+                __syncwarp();                                            // before lane 0 arrives for K
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     const int use = 2 * j + v, slot = use % kSlots;
@@ -537,13 +542,12 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (lane == 0) fail(6);
                 __syncwarp();
             }
-            if (*abort_flag) {
-                // let this CTA's copies land before its shared memory is released
-                mbar_wait(bars + B_Q, 0, kDrainBudget);
-                if (patching) mbar_wait(bars + B_FIX, (uint32_t)(fixes & 1), kDrainBudget);
-                for (int s = max(0, done - kSlots); s < done; ++s)
-                    mbar_wait(bars + B_FULL + s % kSlots, (uint32_t)(s / kSlots & 1), kDrainBudget);
-            }
+            // This CTA's copies land before its shared memory is released, also when another warp gives
+            // up on one after this point.
+            mbar_wait(bars + B_Q, 0, kDrainBudget);
+            if (patching) mbar_wait(bars + B_FIX, (uint32_t)(fixes & 1), kDrainBudget);
+            for (int s = max(0, done - kSlots); s < done; ++s)
+                mbar_wait(bars + B_FULL + s % kSlots, (uint32_t)(s / kSlots & 1), kDrainBudget);
         }
         __syncwarp();
         }

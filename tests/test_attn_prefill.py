@@ -275,6 +275,28 @@ def test_timeout_is_reported():
            lambda n: seen_by([700, 90][n], [0, 300][n]))
 
 
+@pytest.mark.parametrize("budget", [1, 8, 65, 68, 72, 80])
+def test_waits_that_run_out_midway(budget):
+    """With few polls allowed some waits give up and others do not: the call is right or reports the
+    timeout, and the next one is right."""
+    q, kv, cu, pos0, ks, vs = make([700, 90], [0, 300], 8, 2, 128, 16, BF)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    old = gdn.gdn_set_wait_budget(budget)
+    try:
+        results = [gdn.gdn_attn_prefill(q, kv, cu, pos0, workspace=ws)]
+        status = gdn.gdn_get_device_error(ws)
+    finally:
+        gdn.gdn_set_wait_budget(old)
+    assert status in (gdn.GDN_OK, gdn.GDN_ERR_TIMEOUT)
+    if status == gdn.GDN_ERR_TIMEOUT:
+        results.clear()
+    results.append(gdn.gdn_attn_prefill(q, kv, cu, pos0, workspace=ws))
+    assert gdn.gdn_get_device_error(ws) == gdn.GDN_OK
+    for out, lse in results:
+        verify(out, lse, q, ks, vs, [700, 90], [0, 300], 128 ** -0.5, 0.0,
+               lambda n: seen_by([700, 90][n], [0, 300][n]))
+
+
 def test_graph_replay_and_streams():
     q, kv, cu, pos0, ks, vs = make([500, 130], [0, 64], 8, 2, 128, 16, BF)
     want, want_lse = gdn.gdn_attn_prefill(q, kv, cu, pos0)
