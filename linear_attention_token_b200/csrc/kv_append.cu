@@ -35,10 +35,10 @@ struct AppendParams {
     int split_shift;                             // 2^split_shift warps share a token
 };
 
-// Angle p * f in half turns of pi, in [-1, 1]: the product of a 32-bit position and a 24-bit
+// Angle p * f in half turns of pi, in [-1, 1]: the product of a 33-bit position and a 24-bit
 // frequency loses at most its last bits in a double, and is reduced there by a two-part 2 pi (Cody
 // and Waite).
-__device__ __forceinline__ float half_turns(int p, float f) {
+__device__ __forceinline__ float half_turns(long long p, float f) {
     const double x = (double)p * (double)f;
     const double n = rint(x * 0.15915494309189535);
     return (float)(fma(-n, 2.4492935982947064e-16, fma(-n, 6.283185307179586, x)) * 0.3183098861837907);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 6 : 5) kv_append_kerne
     if (p.pos0) pos += __ldg(p.pos0 + n);
     const int row = cache_row(p.cache, n, pos);
     for (int i = lane; i < p.half; i += 32) {
-        const int at = p.rope_pos ? __ldg(p.rope_pos + axis_of(p, i) * p.T_total + t) : (int)pos;
+        const long long at = p.rope_pos ? __ldg(p.rope_pos + axis_of(p, i) * p.T_total + t) : pos;
         float s, c;
         sincospif(half_turns(at, __ldg(p.inv_freq + i)), &s, &c);
         trig[i] = make_float2(c, s);

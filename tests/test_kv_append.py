@@ -126,6 +126,24 @@ def test_far_positions():
     assert close(got, want, tol + 2.0 ** -21 * tol.amax() * 2.0 ** 20, torch.float32)
 
 
+def test_positions_past_32_bits():
+    """Tokens behind the last 32-bit position are not in the cache; their queries are rotated there all
+    the same, and not at a position that wrapped."""
+    d, half, T = 64, 32, 5
+    kc, vc, table = cache(1, 16, 1, d, 16, torch.float32, 0)
+    kv = gdn.PagedKV(kc, vc, table)
+    q = normal((T, 1, d), torch.float32, 1)
+    # frequencies of few bits, so that position x frequency is exact in 64 bits
+    freq = (2.0 ** -torch.arange(half, dtype=torch.float64)).float().to(DEV)
+    start = (1 << 31) - 3
+    out = gdn.gdn_kv_append(q, q, kv, None, torch.tensor([start], dtype=torch.int32, device=DEV), q=q,
+                            inv_freq=freq)
+    at = start + torch.arange(T, device=DEV).double()
+    want, tol = rotated(q, at[:, None] * freq.double(), half)
+    assert close(out, want, tol, torch.float32)
+    assert bool(torch.isnan(kc).all()) and bool(torch.isnan(vc).all())
+
+
 def test_strided_projection_and_in_place():
     """q, k, v as slices of one fused projection; q rotated in place where it is contiguous."""
     H_q, H_kv, d, T = 4, 2, 128, 50
