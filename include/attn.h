@@ -32,7 +32,7 @@
  *
  * Ownership and errors follow gdn.h: the caller owns every buffer (device memory unless
  * stated); nothing allocates, frees or synchronises; argument checks run on the host and
- * return before anything is enqueued.
+ * return before anything is enqueued.  Outputs overlap no input, except q_out as stated below.
  */
 #ifndef LIBGDN_ATTN_H
 #define LIBGDN_ATTN_H
@@ -101,7 +101,8 @@ size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, int32_t H_
 /* Decode.  Query j of sequence n sits at position p = q_pos[n] + j and sees the tokens
  * 0 <= t <= p, with window > 0 only those with t > p - window.
  *   q, out   : [num_seqs, n_queries, H_q, d], 1 <= n_queries <= GDN_ATTN_MAX_QUERIES
- *   q_pos    : DEVICE int32 [num_seqs]; negative for an idle slot (its queries see nothing)
+ *   q_pos    : DEVICE int32 [num_seqs]; a query at a negative position sees nothing, so an idle
+ *              slot has q_pos = -n_queries
  *   lse      : [num_seqs, n_queries, H_q] fp32 or NULL
  * The tokens' keys and values, the queries' own among them, are in the cache already.
  * (Many drafted tokens of wide groups run on gdn_attn_prefill's bf16 kernel, with its bounded
