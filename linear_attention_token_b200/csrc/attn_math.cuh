@@ -67,10 +67,6 @@ inline Scoring scoring(float scale, float cap) {
     s.cap2 = cap * kLog2e;
     return s;
 }
-// cap2 tanh(y) as 1 - 2 / (1 + e^{2y}): off by a few 2^-24 of the cap
-__device__ __forceinline__ float capped_exp2(float y, float cap2) {
-    return cap2 * (1.f - __fdividef(2.f, 1.f + ex2(y * (2.f * kLog2e))));
-}
 // cap2 tanh(y) for |y| <= 1, by the polynomial: off by a few 2^-24 of itself
 __device__ __forceinline__ float capped_near2(float y, float cap2) {
     const float t = y * y;
@@ -78,6 +74,12 @@ __device__ __forceinline__ float capped_near2(float y, float cap2) {
 #pragma unroll
     for (int i = 4; i >= 0; --i) r = fmaf(r, t, tanh_r<5>(i));
     return cap2 * (y * r);
+}
+// cap2 tanh(y) for any y: beyond 1 as 1 - 2 / (1 + e^{2y}), which is off by a few 2^-24 of the cap and
+// so would leave nothing of a score far below a large one
+__device__ __forceinline__ float capped2(float y, float cap2) {
+    const float by_exp = cap2 * (1.f - __fdividef(2.f, 1.f + ex2(y * (2.f * kLog2e))));
+    return fabsf(y) <= 1.f ? capped_near2(y, cap2) : by_exp;
 }
 // N dot products of each lane to scores, in place; the warp takes the polynomial when none of its
 // scores passes the cap.  The whole warp calls it.
@@ -91,7 +93,7 @@ __device__ __forceinline__ void score2(float (&x)[N], const Scoring &s) {
     for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(x[i]));
     if (__any_sync(0xffffffffu, far > 1.f)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = capped_exp2(x[i], s.cap2);
+        for (int i = 0; i < N; ++i) x[i] = capped2(x[i], s.cap2);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = capped_near2(x[i], s.cap2);

@@ -49,16 +49,22 @@ constexpr int kTile = kPrefillTile;        // query rows of a tile, tokens of a 
 constexpr uint32_t kPollNs = 2000, kDrainBudget = GDN_DEFAULT_WAIT_BUDGET;
 constexpr float kLazy = 8.f;               // growth of a row maximum (base 2) that O may lag
 
-// cap2 tanh(y) + add, by the polynomial of degree DEG
-template <int DEG>
-__device__ __forceinline__ float2 capped_near_add2(float2 y, float cap2, float2 add) {
-    const float2 t = mul2(y, y);
-    float2 r = make_float2(tanh_r<DEG>(DEG) * cap2, tanh_r<DEG>(DEG) * cap2);
+// cap2 tanh(k s) + add for two s, by the polynomial of degree DEG whose coefficients carry k and cap2
+template <int DEG> struct Near {
+    float c[DEG + 1];
+    __device__ __forceinline__ Near(float k, float cap2) {
+        float f = k * cap2;
 #pragma unroll
-    for (int i = DEG - 1; i >= 0; --i)
-        r = fma2(r, t, make_float2(tanh_r<DEG>(i) * cap2, tanh_r<DEG>(i) * cap2));
-    return fma2(y, r, add);
-}
+        for (int i = 0; i <= DEG; ++i, f *= k * k) c[i] = tanh_r<DEG>(i) * f;
+    }
+    __device__ __forceinline__ float2 operator()(float2 s, float2 add) const {
+        const float2 t = mul2(s, s);
+        float2 r = make_float2(c[DEG], c[DEG]);
+#pragma unroll
+        for (int i = DEG - 1; i >= 0; --i) r = fma2(r, t, make_float2(c[i], c[i]));
+        return fma2(s, r, add);
+    }
+};
 // the larger of three
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -234,25 +240,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
             const bool whole = k0 >= lo_max && k0 + kTile <= hi_min &&
                                (pm.x & pm.y & pm.z & pm.w) == 0xffffffffu;
-            // tanh(y) by a polynomial on the FMA pipe while no score of the warp's rows passes the
-            // cap (|y| <= 1), a shorter one while none passes half of it, else by exponentials (two
-            // more per score on the busiest pipe)
-            bool near = false, nearer = false;
-            if (CAP) {
-                if (whole) {
-                    float far = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
-                    near = __all_sync(0xffffffffu, far * k2 <= 1.f);
-                    nearer = __all_sync(0xffffffffu, far * k2 <= 0.5f);
-                }
-                if (!near) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = capped_exp2(s[c] * k2, cap2);
-                }
-            }
+            uint32_t live[4] = {pm.x, pm.y, pm.z, pm.w};
             if (!whole) {
-                const uint32_t pw[4] = {pm.x, pm.y, pm.z, pm.w};
                 const int a = lo - k0, z = hi - k0;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -260,11 +249,40 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const int b0 = min(max(a - 32 * w, 0), 32), b1 = min(max(z - 32 * w, 0), 32);
                     const uint32_t below1 = b1 == 32 ? 0xffffffffu : (1u << b1) - 1u;
                     const uint32_t below0 = b0 == 32 ? 0xffffffffu : (1u << b0) - 1u;
-                    const uint32_t live = pw[w] & below1 & ~below0;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        s[32 * w + c] = (live >> c) & 1 ? s[32 * w + c] : -INFINITY;
+                    live[w] &= below1 & ~below0;
                 }
+            }
+            // tanh(y) by a polynomial on the FMA pipe while no live score of the warp's rows passes the
+            // cap (|y| <= 1), a shorter one while none passes half of it, else by exponentials (two
+            // more per score on the busiest pipe). In whole tiles the polynomial runs beside the
+            // weights' exponentials, with the scale in its coefficients (404 us for prompts of 8191
+            // tokens behind 2800-4000, 16 x 4 heads, capped; 412 with a product more per score).
+            bool near = false, nearer = false;
+            if (CAP) {
+                float far = 0.f;
+                if (whole) {
+                    far = p.far_from;                                    // see launch_attn_prefill
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        far = fmaxf(far, (live[c >> 5] >> (c & 31)) & 1 ? fabsf(s[c]) : 0.f);
+                }
+                near = __all_sync(0xffffffffu, far * k2 <= 1.f);
+                nearer = whole && __all_sync(0xffffffffu, far * k2 <= 0.5f);
+                if (!near) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = capped2(s[c] * k2, cap2);
+                } else if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = capped_near2(s[c] * k2, cap2);
+                }
+                near = near && whole;
+            }
+            if (!whole) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] = (live[c >> 5] >> (c & 31)) & 1 ? s[c] : -INFINITY;
             }
             float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -323,11 +341,13 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 for (int x = 0; x < 16; ++x) w16[x] = weights(96 + 2 * x);
                 tmem_st16(s_at + 48, w16);
             };
-            if (CAP && nearer)
-                all_weights([&](float2 x) { return capped_near_add2<3>(mul2(x, make_float2(k2, k2)), cap2, sh); });
-            else if (CAP && near)
-                all_weights([&](float2 x) { return capped_near_add2<5>(mul2(x, make_float2(k2, k2)), cap2, sh); });
-            else
+            if (CAP && nearer) {
+                const Near<3> cap(k2, cap2);
+                all_weights([&](float2 x) { return cap(x, sh); });
+            } else if (CAP && near) {
+                const Near<5> cap(k2, cap2);
+                all_weights([&](float2 x) { return cap(x, sh); });
+            } else
                 all_weights([&](float2 x) { return fma2(x, kk, sh); });
             l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
             publish(1);
@@ -478,6 +498,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ====================================================================== loads
         const int ps = 1 << p.cache.page_shift, box = ps < kTile ? ps : kTile;
         const int boxes = kTile / box;
+        const bool leader = elect_one();
         if (nt > 0) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(bars + B_Q, 2 * L::kTileBytes);
@@ -514,10 +535,15 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     uint64_t *bar = bars + (fix ? B_FIX : B_FULL + slot);
                     if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
-                    if (src >= 0)
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(dst + h * L::kHalf + lane * box * 128, v ? &tm_v : &tm_k, bar,
-                                        64 * h, hk, src);
+                    // the whole warp walks the boxes and one lane issues, as for the products (pages of 16
+                    // tokens: 400 against 404 us with a lane to a box)
+                    for (int b = 0; b < boxes; ++b) {
+                        const int at = __shfl_sync(0xffffffffu, src, b);
+                        if (at >= 0 && leader)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(dst + h * L::kHalf + b * box * 128, v ? &tm_v : &tm_k, bar,
+                                            64 * h, hk, at);
+                    }
                     if (fix) {
                         patching = true;
                         ok = wait(B_FIX, fixes);

@@ -163,6 +163,10 @@ cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int
     p.window = window;
     p.pack_shift = s.pack_shift;
     p.score = scoring(scale, cap);
+    // The bf16 kernel's polynomial for capped scores carries powers of scale / cap up to the 11th in its
+    // coefficients; outside this range (a cap of 360 and more at a scale of 0.09) they would leave fp32.
+    const float k = fabsf(p.score.mul);
+    p.far_from = k >= 0x1p-12f && k <= 0x1p10f ? 0.f : INFINITY;
     p.err = static_cast<DeviceError *>(workspace);
     p.budget = budget;
     p.blocks = s.blocks;

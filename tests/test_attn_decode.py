@@ -181,6 +181,17 @@ def test_scale_of_any_sign_and_far_caps(scale, softcap, dtype):
     assert none is None and torch.equal(again, out)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("softcap,far", [(1e3, 1.0), (1e6, 1.0), (2e4, 3e4), (1e6, 2e6)])
+def test_large_caps(softcap, far, dtype):
+    """A large cap changes small scores by nothing, also beside a head whose scores pass it."""
+    q, pos, kv, ks, vs = make([300, 20], 2, 4, 2, 64, 16, dtype)
+    q[:, :, 1] *= far
+    out, lse = gdn.gdn_attn_decode(q, pos, kv, softcap=softcap)
+    verify(out, lse, q, ks, vs, lambda n, j: torch.arange([300, 20][n] - 1 + j, device=DEV), 0.125,
+           softcap, dtype)
+
+
 def test_peaked_scores():
     """Scores of hundreds, of both signs: one key decides, and the running maximum jumps."""
     q, pos, kv, ks, vs = make([2000], 1, 8, 2, 128, 16, torch.bfloat16, by=60.0)

@@ -160,6 +160,16 @@ def test_scale_of_any_sign(scale, softcap):
     verify(out, lse, q, ks, vs, [150], [20], scale, softcap, lambda n: seen_by(150, 20))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("softcap,far", [(1e3, 1.0), (1e6, 1.0), (2e4, 3e4), (1e6, 2e6), (12.0, 1.0), (5e3, 1e3)])
+def test_large_caps(softcap, far, dtype):
+    """A large cap changes small scores by nothing, also beside a head whose scores pass it."""
+    q, kv, cu, pos0, ks, vs = make([150], [300], 4, 2, 64, 16, dtype)
+    q[:, 1] *= far
+    out, lse = gdn.gdn_attn_prefill(q, kv, cu, pos0, softcap=softcap)
+    verify(out, lse, q, ks, vs, [150], [300], 0.125, softcap, lambda n: seen_by(150, 300))
+
+
 def test_growing_maxima():
     """Scores that rise by hundreds along the sequence: O is rescaled again and again; and scores
     that fall, where it never is."""
