@@ -253,15 +253,15 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             // tanh(y) by a polynomial on the FMA pipe while no live score of the warp's rows passes the
-            // cap (|y| <= 1), a shorter one while none passes half of it, else by exponentials (two
-            // more per score on the busiest pipe). In whole tiles the polynomial runs beside the
-            // weights' exponentials, with the scale in its coefficients (404 us for prompts of 8191
-            // tokens behind 2800-4000, 16 x 4 heads, capped; 412 with a product more per score).
+            // cap (|y| <= 1), a shorter one while none passes half of it, else by exponentials too (two
+            // more per score on the busiest pipe: 383 against 185 us for 2 x 1500 tokens behind 4000, 16 x
+            // 4 heads; 155 without a cap). In whole tiles the polynomial runs beside the weights'
+            // exponentials, with the scale in its coefficients (8191 tokens behind 2800-4000, 16 x 4 heads:
+            // 404 us, 412 with a product more per score).
             bool near = false, nearer = false;
             if (CAP) {
                 float far = 0.f;
                 if (whole) {
-                    far = p.far_from;                                    // see launch_attn_prefill
 #pragma unroll
                     for (int c = 0; c < 128; c += 2) far = max3(far, fabsf(s[c]), fabsf(s[c + 1]));
                 } else {
@@ -269,15 +269,19 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     for (int c = 0; c < 128; ++c)
                         far = fmaxf(far, (live[c >> 5] >> (c & 31)) & 1 ? fabsf(s[c]) : 0.f);
                 }
-                near = __all_sync(0xffffffffu, far * k2 <= 1.f);
-                nearer = whole && __all_sync(0xffffffffu, far * k2 <= 0.5f);
-                if (!near) {
+                near = __all_sync(0xffffffffu, far * k2 <= p.near_at);
+                nearer = whole && __all_sync(0xffffffffu, far * k2 <= p.nearer_at);
+                // in place, two at a time
+                auto cap_all = [&](auto &&cap) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = capped2(s[c] * k2, cap2);
-                } else if (!whole) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = capped_near2(s[c] * k2, cap2);
-                }
+                    for (int c = 0; c < 128; c += 2) {
+                        const float2 x = cap(mul2(make_float2(s[c], s[c + 1]), make_float2(k2, k2)));
+                        s[c] = x.x;
+                        s[c + 1] = x.y;
+                    }
+                };
+                if (!near) cap_all([&](float2 y) { return capped2(y, cap2); });
+                else if (!whole) cap_all([&](float2 y) { return capped_near2(y, cap2); });
                 near = near && whole;
             }
             if (!whole) {
@@ -291,7 +295,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
             float mx = max3(fmaxf(mx4[0], s[124]), fmaxf(mx4[1], s[125]),
                             fmaxf(fmaxf(mx4[2], s[126]), fmaxf(mx4[3], s[127])));
-            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped_near2(mx * k2, cap2) : mx * k2;
+            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped_near2(make_float2(mx * k2, 0.f), cap2).x : mx * k2;
             const bool grow = mx > m + kLazy;                            // also when m is -inf
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2(m - mx) : 1.f;                // 0 from -inf
@@ -344,8 +348,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (CAP && nearer) {
                 const Near<3> cap(k2, cap2);
                 all_weights([&](float2 x) { return cap(x, sh); });
-            } else if (CAP && near) {
+            } else if (CAP && near && p.nearer_at > 0.f) {
                 const Near<5> cap(k2, cap2);
+                all_weights([&](float2 x) { return cap(x, sh); });
+            } else if (CAP && near) {
+                const Near<2> cap(k2, cap2);
                 all_weights([&](float2 x) { return cap(x, sh); });
             } else
                 all_weights([&](float2 x) { return fma2(x, kk, sh); });

@@ -20,7 +20,7 @@ struct AttnPrefillParams {
     bool heads_first;                      // order of the CTAs
     int pack_shift;                        // rows of a tile: token r >> pack_shift, head the rest
     Scoring score;
-    float far_from;                        // 0; infinity keeps whole tiles from the cap's polynomial
+    float near_at, nearer_at;              // largest |score / cap| of the cap's two polynomials
     DeviceError *err;
     uint32_t budget;
     long long blocks;                      // (block, head) pairs, as prefill_shape counts them

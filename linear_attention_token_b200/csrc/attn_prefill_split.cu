@@ -163,10 +163,13 @@ cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int
     p.window = window;
     p.pack_shift = s.pack_shift;
     p.score = scoring(scale, cap);
-    // The bf16 kernel's polynomial for capped scores carries powers of scale / cap up to the 11th in its
-    // coefficients; outside this range (a cap of 360 and more at a scale of 0.09) they would leave fp32.
+    // The bf16 kernel's polynomials for capped scores carry powers of k = scale / cap in their coefficients:
+    // up to the 11th (degree 5, |y| <= 1, and degree 3, |y| <= 1/2) where those stay inside fp32; for
+    // larger caps (from 360 at a scale of 0.09) the 5th (degree 2, |y| <= 1/8).
     const float k = fabsf(p.score.mul);
-    p.far_from = k >= 0x1p-12f && k <= 0x1p10f ? 0.f : INFINITY;
+    const bool all = k >= 0x1p-12f && k <= 0x1p10f;
+    p.near_at = all ? 1.f : k >= 0x1p-24f && k <= 0x1p10f ? 0.125f : -1.f;
+    p.nearer_at = all ? 0.5f : -1.f;
     p.err = static_cast<DeviceError *>(workspace);
     p.budget = budget;
     p.blocks = s.blocks;
