@@ -604,7 +604,7 @@ def gdn_attn_decode(q, q_pos, kv: PagedKV, *, scale: Optional[float] = None, sof
                     stream=None):
     """Attention of the newest tokens over the whole cache: q [N, T, H_q, d] (query j of
     sequence n at position q_pos[n] + j, seeing the tokens at or before it, with window > 0 only
-    the last `window` of them), q_pos int32 [N].  scale None is d^-0.5; softcap > 0 caps scores
+    the last `window` of them; none at a negative position: an idle slot has q_pos -T), q_pos int32 [N].  scale None is d^-0.5; softcap > 0 caps scores
     by a tanh.  Returns (out, lse [N, T, H_q] float32 or None)."""
     return _run("gdn_attn_decode", _marshal().decode, kv, stream,
                 (q, q_pos, None, 0, scale, softcap, window, out, lse, want_lse, workspace))
@@ -625,7 +625,8 @@ def gdn_qsa_attn_decode(q, q_pos, kv: PagedKV, token_idx, *, recent: int = 0,
 
 def gdn_attn_prefill_workspace_size(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
                                     varlen: bool = True) -> int:
-    return int(lib().gdn_attn_prefill_workspace_size(ctypes.byref(kv._struct), int(varlen), num_seqs, T_total, H_q))
+    return int(lib().gdn_attn_prefill_workspace_size(ctypes.byref(kv._struct), int(varlen), num_seqs,
+                                                     T_total, H_q))
 
 
 def attn_prefill_workspace(kv: PagedKV, num_seqs: int, T_total: int, H_q: int,
@@ -646,7 +647,7 @@ def gdn_attn_prefill(q, kv: PagedKV, cu_seqlens=None, pos0=None, *, prefix_len=N
     pos0[n] + i (pos0 None: 0) and sees the tokens at or before it, with window > 0 only the last
     `window` of them, with prefix_len int32 [N] also those before prefix_len[n].  A workspace
     (attn_prefill_workspace; None takes one for the call) records a device-side timeout for
-    gdn_get_device_error and lets few rows behind a long context use all SMs.  Returns (out, lse [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are
-    left alone."""
+    gdn_get_device_error and lets few rows behind a long context use all SMs.  Returns (out, lse
+    [T_total, H_q] or [B, T, H_q] float32, or None); rows behind the last sequence are left alone."""
     return _run("gdn_attn_prefill", _marshal().prefill, kv, stream,
                 (q, cu_seqlens, pos0, prefix_len, scale, softcap, window, out, lse, want_lse, workspace))

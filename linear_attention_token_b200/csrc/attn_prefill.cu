@@ -14,17 +14,26 @@
 //
 // Per pair of 128 x 128 tiles (d = 128) the tensor pipe needs 2048 cycles and the 2 x 16384
 // exponentials, at 16 per cycle and SM, 2048 as well: the two are balanced, and what is lost is
-// what does not overlap.
+// what does not overlap. A pair takes about 3100 cycles: of a tile's turn (loads of S, maxima, 1024
+// cycles of exponentials, then PV and the next S) only the other tile's products lie beside it, since
+// two S, two O fill TMEM and S(j+1) cannot start before PV(j) has read P(j). (A quarter of the
+// exponentials as polynomials on the FMA pipe made it longer, 126 -> 133 us at 2 x 4096 tokens.)
 //  - warps 0-3, 4-7: the softmax of tile A, B; a thread owns a row (TMEM lane), so maxima and
 //    sums need no exchange.  P goes back to TMEM over the first half of S, as the A operand of PV.
 //    O is rescaled only when a row's maximum grew by more than 2^8 (until then P and l simply use
 //    the old one): after the first tiles that is rare, so no warps are kept for it.
-//  - warp 8: issues the products.  PV(j) and S(j+1) of a tile go out together;
-//    S(j+1) overwrites the columns P(j) was in, after PV(j) read them (one thread's products run
-//    in order).
-//  - warp 10 (9 and 11 only fill the warpgroup): loads.  K and V tiles of 128 tokens alternate through a ring, gathered page by page
-//    with TMA; tokens that are absent are left out of the softmax by a mask, and their V rows (and
+//  - warp 8: issues the products.  PV(j) and S(j+1) of a tile go out together; S(j+1) overwrites the
+//    columns P(j) was in, after PV(j) read them (one thread's products run in order).
+//  - warp 10: loads.  K and V tiles of 128 tokens alternate through a ring of four, gathered page by
+//    page with TMA; tokens that are absent are left out of the softmax by a mask, and their V rows (and
 //    those past the sequence) are zeroed, so nothing a dead row holds reaches a product.
+//  - warps 9 and 11 fill the warpgroup, whose registers the softmax takes over.
+//
+// Measured: one prompt of 16,384 tokens x 16 heads (2 key heads) 855-910 us, 1.21-1.29 PFLOP/s on a
+// chip at its power cap (cuBLAS there: 1.40); 2 x 4096 tokens 126 us, 1.09 PFLOP/s, tensor pipe active
+// 49%; 8191 ragged tokens behind 2800-4000, 16 x 4 heads, capped, pages of 16: 398 us. Of these the cap
+// takes 60 (the FMA pipe), pages of 16 rather than 128 tokens 30 (eight loads to a tile half), and
+// unequal blocks on 148 SMs 40.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -427,8 +436,9 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (warp == 8) {
             // =============================================================== products
             // Tile A's and tile B's turns alternate, which keeps the two softmax warpgroups half a period
-            // apart (one issuing warp for each lets them fall into step).  The whole warp walks this code and one elected lane issues: descriptors then
-            // stay in uniform registers (issued from a divergent thread, a product took 60-100 cycles).
+            // apart (one issuing warp for each lets them fall into step).  The whole warp walks this code
+            // and one elected lane issues: descriptors then stay in uniform registers (issued from a
+            // divergent thread, a product took 60-100 cycles).
             const uint32_t neg = p.score.mul < 0.f ? 1u << 14 : 0u;      // the softmax takes |mul|
             const uint32_t id_s = idesc_bf16(128, 128, false, false) | neg;
             const uint32_t id_o = idesc_bf16(128, D, false, true);
