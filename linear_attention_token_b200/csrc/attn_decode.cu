@@ -18,6 +18,8 @@
 //    others go to the workspace (at most two per CTA), and attn_join_kernel, launched beside this
 //    one, joins them.  (The last CTA of a unit joining in this kernel was slower on every size: one
 //    CTA's fences, atomics and cold code at the end cost more than a second grid.)
+//    Short calls of few units take a cluster of CTAs to a unit instead, which join their parts in
+//    shared memory and need no second grid (cluster_for).
 //  - bf16: a warp owns 16 query rows as one mma.sync m16n8k16 row tile.  With few rows the
 //    product is far from the tensor pipe's limit, so what counts is that loads never pause:
 //    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
@@ -28,8 +30,8 @@
 // bf16 320 us, 6.7 TB/s; 64 ragged ones of 2000 to 16,384 tokens x 8 heads, two drafted tokens each, 356 us,
 // 6.6 TB/s; one of 262,144 tokens x 2 heads 53 us, 5.1 TB/s; fp32, 64 x 4096 tokens x 2 heads, d = 128:
 // 87 us, 6.2 TB/s with one row a head, 126 with eight, which are bound by their FMAs. Lists of 2048 tokens
-// for 32 x 4 drafted queries: 55 us, 4.9 TB/s; 4 x 1024 tokens: 9.3 us, mostly the two launches and the
-// chain position -> page table -> keys.
+// for 32 x 4 drafted queries: 55 us, 4.9 TB/s; 4 x 1024 tokens: 6.6 us, mostly the launch and the chain
+// position -> page table -> keys.
 #include <math.h>
 #include <stdint.h>
 
@@ -43,6 +45,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
+constexpr int kMostCluster = 16;
 constexpr int kLoad = 16;                  // keys one warp loads per step
 constexpr int kStep = kWarps * kLoad;      // keys per step of a CTA
 // Growth of a row's maximum (base 2) that its sums may lag: until then the old one serves, and
@@ -466,7 +469,7 @@ struct Layout {
     static constexpr int kStageBytes = kStep * kRowBytes;              // K or V of one step
     static constexpr int kRing = kStages * 2 * kStageBytes;
     // the join of the CTA's teams reuses the ring
-    static constexpr int kJoin = kTeams * ROWS::kRows * (D + 2) * 4;
+    static constexpr int kJoin = (kTeams + 1) * ROWS::kRows * (D + 2) * 4;    // (+ 1: the CTA's part, in a cluster)
     static constexpr int kExtra = sizeof(typename ROWS::E) == 4 ? (ROWS::kRows * D + kWarps * ROWS::kRows * kLoad) * 4 : 0;
     static constexpr int kMask = kStages * kWarps * 4;
     static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
@@ -540,7 +543,39 @@ __device__ __forceinline__ void finish(const DecodeParams &p, const Unit &u, int
     if (c == 0 && p.lse) p.lse[rh] = s.l > 0.f ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
 }
 
-template <class ROWS, int D, bool LIST>
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// address of CTA `rank`'s copy of what lies at addr in this CTA's shared memory
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
+    return x;
+}
+
+// CLUSTER: a cluster of CTAs takes a unit, and they join their parts in shared memory.
+template <class ROWS, int D, bool LIST, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using E = typename ROWS::E;
@@ -552,14 +587,23 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     float *extra = reinterpret_cast<float *>(sm + L::kBody);
     uint32_t *masks = reinterpret_cast<uint32_t *>(sm + L::kBody + L::kExtra);   // [stage][warp]
 
-    pdl_trigger();
     // all steps, and where this CTA's stretch begins
     const int cta = blockIdx.x;
-    if (tid == 0 && !p.by_unit) p.rec[cta].parts = 0;
-    long long W, begin, end;
-    int G, n, sub, step;
+    if (!CLUSTER) {
+        pdl_trigger();
+        if (tid == 0 && !p.by_unit) p.rec[cta].parts = 0;
+    }
+    long long W = 0, begin = 0, end;
+    int G = 0, n, sub, step;
     Span sp;
-    if (LIST) {                            // every unit has the same steps
+    if (CLUSTER) {                         // a unit's steps from `step` on
+        const int size = cluster_size(), rank = cluster_rank(), unit = cta / size;
+        n = unit / p.units_per_seq;
+        sub = unit - n * p.units_per_seq;
+        sp = span_of<LIST>(p, n);
+        step = (int)((long long)sp.steps * rank / size);
+        end = (long long)sp.steps * (rank + 1) / size - step;    // may be 0: an empty part
+    } else if (LIST) {                     // every unit has the same steps
         sp = span_of<LIST>(p, 0);
         W = (long long)p.N * p.units_per_seq * sp.steps;
         G = (int)(W < (long long)gridDim.x ? W : gridDim.x);
@@ -605,12 +649,12 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         sub = (int)(found[1] / sp.steps);
         step = (int)(found[1] - (long long)sub * sp.steps);
     }
-    end = stretch(W, G, cta + 1);
+    if (!CLUSTER) end = stretch(W, G, cta + 1);
 
     ROWS rows;
     const int team = warp / TEAM;
     const uint32_t ring = smem_addr(sm);
-    for (long long at = begin; at < end;) {
+    for (long long at = begin; CLUSTER || at < end;) {
         const Unit u = unit_of<LIST>(p, n, sub);
         const long long pos = __ldg(p.q_pos + n);
         const int count = (int)min((long long)(sp.steps - step), end - at);
@@ -655,6 +699,32 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
         float2 *sml = reinterpret_cast<float2 *>(so + L::kTeams * ROWS::kRows * D);
         rows.put(so + team * ROWS::kRows * D, sml + team * ROWS::kRows);
         __syncthreads();
+        if constexpr (CLUSTER) {
+            // this CTA's part [rows][D], then m and l, behind the teams' ones; each CTA joins some rows
+            constexpr int R = ROWS::kRows;
+            float *po = so + L::kTeams * R * (D + 2);
+            float2 *pml = reinterpret_cast<float2 *>(po + R * D);
+            const int live_rows = min(R, p.rows - u.rb * R);
+            for (int i = tid; i < live_rows * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), c = 4 * (i % (D / 4));
+                const Sums s = sum_parts<L::kTeams>(
+                    L::kTeams, [&](int t) { return sml[t * R + r]; },
+                    [&](int t) { return *reinterpret_cast<const float4 *>(so + (t * R + r) * D + c); });
+                *reinterpret_cast<float4 *>(po + r * D + c) = s.o;
+                if (c == 0) pml[r] = make_float2(s.m, s.l);
+            }
+            cluster_sync();
+            const int size = cluster_size(), c = 4 * (tid % (D / 4));
+            for (int r = (int)cluster_rank() + size * (tid / (D / 4)); r < live_rows; r += size * (kThreads / (D / 4))) {
+                const uint32_t at_o = smem_addr(po + r * D + c), at_ml = smem_addr(pml + r);
+                const Sums s = sum_parts<kMostCluster>(
+                    size, [&](int i) { return peer_load2(peer_addr(at_ml, i)); },
+                    [&](int i) { return peer_load4(peer_addr(at_o, i)); });
+                finish<E, D, LIST>(p, u, u.rb * R + r, c, s);
+            }
+            cluster_sync();                // parts stay until everyone has read them
+            return;
+        }
         const bool whole = count == sp.steps;
         const int slot = at == begin ? 0 : 1;
         const int live_rows = min(ROWS::kRows, p.rows - u.rb * ROWS::kRows);
@@ -786,26 +856,90 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 }
 
 template <class ROWS, int D, bool LIST> PerDevice g_setup;
+// clusters of 2 << i CTAs that run at once on a device
+template <class ROWS, int D, bool LIST> int g_clusters[PerDevice::kMaxDevices][4];
+
+template <class ROWS, int D, bool LIST>
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *cluster, long long units, int size,
+                                  cudaStream_t stream) {
+    cluster->id = cudaLaunchAttributeClusterDimension;
+    cluster->val.clusterDim.x = size;
+    cluster->val.clusterDim.y = cluster->val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<ROWS, D>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = cluster;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <class ROWS, int D, bool LIST> cudaError_t setup() {
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    const auto line = attn_decode_kernel<ROWS, D, LIST, false>, in_cluster = attn_decode_kernel<ROWS, D, LIST, true>;
+    constexpr int smem = Layout<ROWS, D>::kSmem;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(line, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(in_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(in_cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = cluster_config<ROWS, D, LIST>(&attr, 1, 2 << i, nullptr);
+        e = cudaOccupancyMaxActiveClusters(&g_clusters<ROWS, D, LIST>[dev][i], in_cluster, &cfg);
+    }
+    return e;
+}
+
+// Most steps that a unit of the call can have.
+template <bool LIST> long long most_steps(const DecodeParams &p) {
+    if (LIST) return (p.list_len + kStep - 1) / kStep + (p.recent + kStep - 1) / kStep;
+    long long tokens = (long long)p.cache.max_pages << p.cache.page_shift;
+    if (p.window > 0 && tokens > (long long)p.window + p.T + kStep) tokens = (long long)p.window + p.T + kStep;
+    return (tokens + kStep - 1) / kStep;
+}
+
+// CTAs of a cluster for each unit, or 1: the even split and its join. A cluster saves the second grid
+// and the parts' way through memory, about 3 us or 5 steps, but gives every unit the same CTAs whatever
+// its length, and some SMs none. (bf16, 16 x 2 heads, even split / cluster: 4 sequences of 1024 tokens 9.5 /
+// 6.6 us; lists of 2048 for 8 sequences 11.1 / 10.1, for 16 14.5 / 11.1, for 32 20.2 / 16.0, for 74 36.8 /
+// 33.2; but for 37 19.8 / 22.4, and 1 sequence of 16,384 tokens 13.4 / 15.9.)
+template <class ROWS, int D, bool LIST> int cluster_for(const DecodeParams &p, long long units, int grid) {
+    int dev;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    const long long steps = most_steps<LIST>(p);
+    // (16 CTAs are worth their wider barrier for long units or few: 8 units of 16 steps 7.1 us, with 8 6.6)
+    int i = steps > 32 || units <= 4 ? 3 : 2;
+    while (i >= 0 && units > g_clusters<ROWS, D, LIST>[dev][i]) --i;
+    if (i < 0) return 1;
+    const int size = 2 << i;
+    const long long each = (steps + size - 1) / size;
+    // whole cache: the lengths behind the table's are not known, so a long sequence may be alone
+    return each - units * steps / grid <= 5 && (LIST || each <= 8) ? size : 1;
+}
 
 template <class ROWS, int D, bool LIST>
 cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
     constexpr int smem = Layout<ROWS, D>::kSmem;
     int sms = 0;
-    cudaError_t e = g_setup<ROWS, D, LIST>.ensure([] {
-        return cudaFuncSetAttribute(attn_decode_kernel<ROWS, D, LIST>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    }, &sms);
+    cudaError_t e = g_setup<ROWS, D, LIST>.ensure(setup<ROWS, D, LIST>, &sms);
     if (e != cudaSuccess) return e;
     // (fp32 rings of d = 128 leave room for one CTA an SM)
     const int grid = sms * (2 * (smem + 1024) <= 233472 ? kCtasPerSm : 1);
     p.row_blocks = (p.rows + ROWS::kRows - 1) / ROWS::kRows;
     p.units_per_seq = p.cache.H_kv * p.row_blocks * (LIST ? p.T : 1);
     const long long units = (long long)p.N * p.units_per_seq;
+    const int size = cluster_for<ROWS, D, LIST>(p, units, grid);
+    if (size > 1) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = cluster_config<ROWS, D, LIST>(&attr, units, size, stream);
+        return cudaLaunchKernelEx(&cfg, attn_decode_kernel<ROWS, D, LIST, true>, p);
+    }
     p.by_unit = units <= grid;
     p.rec = static_cast<JoinRecord *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.rec + grid);
     p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)grid * 2 * ROWS::kRows);
-    attn_decode_kernel<ROWS, D, LIST><<<grid, kThreads, smem, stream>>>(p);
+    attn_decode_kernel<ROWS, D, LIST, false><<<grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = p.rows < ROWS::kRows ? p.rows : ROWS::kRows;
     // (4 sequences x 2 heads of 1024 tokens: a CTA for each of 296 CTAs and 8 rows 12.3 us a call, for

@@ -131,6 +131,21 @@ def test_token_listed_twice_counts_twice():
     verify(out, lse, q, ks, vs, lambda n, j: idx[0][idx[0] >= 0].long(), 0.125, 0.0, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,H_kv,most", [(1, 1, 4096), (2, 4, 1000), (3, 2, 2048), (30, 1, 1024), (60, 1, 500),
+                                         (60, 2, 500)])
+def test_short_calls_of_few_units(N, H_kv, most, dtype):
+    """Every number of CTAs to a unit, with lengths down to none: some CTAs of a unit have no key."""
+    lens = [most - 37 * n if n % 3 else n for n in range(N)]
+    lens = [max(0, L) for L in lens]
+    T, G = 1, 3
+    q, pos, kv, ks, vs = make(lens, T, G * H_kv, H_kv, 64, 16, dtype)
+    out, lse = gdn.gdn_attn_decode(q, pos, kv)
+    verify(out, lse, q, ks, vs, lambda n, j: torch.arange(lens[n], device=DEV), 0.125, 0.0, dtype)
+    again, _ = gdn.gdn_attn_decode(q, pos, kv)
+    assert torch.equal(again, out)
+
+
 def test_many_ragged_sequences():
     """Units that end anywhere inside a CTA's stretch, idle slots among them."""
     g = torch.Generator().manual_seed(1)
