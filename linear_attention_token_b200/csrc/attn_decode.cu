@@ -38,8 +38,16 @@
 #include "attn_math.cuh"
 #include "device_once.h"
 #include "paged_kv.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
+using sm100::cluster_rank;
+using sm100::cluster_size;
+using sm100::cluster_sync;
+using sm100::ld_cluster2;
+using sm100::ld_cluster4;
+using sm100::map_to_rank;
+
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
@@ -543,37 +551,6 @@ __device__ __forceinline__ void finish(const DecodeParams &p, const Unit &u, int
     if (c == 0 && p.lse) p.lse[rh] = s.l > 0.f ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// address of CTA `rank`'s copy of what lies at addr in this CTA's shared memory
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
-    float4 x;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
-    return x;
-}
-__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
-    float2 x;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
-    return x;
-}
-
 // CLUSTER: a cluster of CTAs takes a unit, and they join their parts in shared memory.
 template <class ROWS, int D, bool LIST, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -713,15 +690,16 @@ attn_decode_kernel(const __grid_constant__ DecodeParams p) {
                 *reinterpret_cast<float4 *>(po + r * D + c) = s.o;
                 if (c == 0) pml[r] = make_float2(s.m, s.l);
             }
+            __syncwarp();
             cluster_sync();
             const int size = cluster_size(), c = 4 * (tid % (D / 4));
             for (int r = (int)cluster_rank() + size * (tid / (D / 4)); r < live_rows; r += size * (kThreads / (D / 4))) {
-                const uint32_t at_o = smem_addr(po + r * D + c), at_ml = smem_addr(pml + r);
                 const Sums s = sum_parts<kMostCluster>(
-                    size, [&](int i) { return peer_load2(peer_addr(at_ml, i)); },
-                    [&](int i) { return peer_load4(peer_addr(at_o, i)); });
+                    size, [&](int i) { return ld_cluster2(map_to_rank(pml + r, i)); },
+                    [&](int i) { return ld_cluster4(map_to_rank(po + r * D + c, i)); });
                 finish<E, D, LIST>(p, u, u.rb * R + r, c, s);
             }
+            __syncwarp();
             cluster_sync();                // parts stay until everyone has read them
             return;
         }

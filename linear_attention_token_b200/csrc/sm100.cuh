@@ -236,6 +236,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
 // shared::cluster address of the same shared-memory location in CTA `rank`
 __device__ __forceinline__ uint32_t map_to_rank(const void *p, uint32_t rank) {
     uint32_t r;
@@ -317,6 +322,18 @@ __device__ __forceinline__ void bulk_wait_read_all() {
 // this thread's committed bulk stores have completed (their writes are performed)
 __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// loads of two and four floats from a shared::cluster address (another CTA's shared memory)
+__device__ __forceinline__ float2 ld_cluster2(uint32_t cluster_addr) {
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(cluster_addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(cluster_addr) : "memory");
+    return x;
 }
 // 32-bit load from a shared::cluster address (another CTA's shared memory)
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
