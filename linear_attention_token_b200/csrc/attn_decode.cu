@@ -864,7 +864,11 @@ template <class ROWS, int D, bool LIST> cudaError_t setup() {
     for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
         cudaLaunchAttribute attr;
         const cudaLaunchConfig_t cfg = cluster_config<ROWS, D, LIST>(&attr, 1, 2 << i, nullptr);
-        e = cudaOccupancyMaxActiveClusters(&g_clusters<ROWS, D, LIST>[dev][i], in_cluster, &cfg);
+        int &most = g_clusters<ROWS, D, LIST>[dev][i];
+        if (cudaOccupancyMaxActiveClusters(&most, in_cluster, &cfg) != cudaSuccess) {
+            most = 0;                      // a size the device does not take
+            cudaGetLastError();
+        }
     }
     return e;
 }

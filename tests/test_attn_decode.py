@@ -312,3 +312,19 @@ def test_other_stream():
     torch.cuda.synchronize()
     for o, l in outs:
         assert torch.equal(o, want) and torch.equal(l, want_lse)
+
+
+def test_calls_at_once():
+    """Calls of every form side by side on four streams, each with its own workspace."""
+    kinds = [make([900, 30, 512], 1, 8, 2, 128, 16, torch.bfloat16), make([9000, 700], 2, 8, 2, 128, 16, torch.bfloat16),
+             make([300] * 9, 4, 16, 1, 128, 16, torch.bfloat16), make([1000, 5], 1, 4, 2, 64, 16, torch.float32)]
+    want = [gdn.gdn_attn_decode(q, pos, kv) for q, pos, kv, _, _ in kinds]
+    streams = [torch.cuda.Stream() for _ in kinds]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for i, (q, pos, kv, _, _) in enumerate(kinds):
+            got.append((i, gdn.gdn_attn_decode(q, pos, kv, stream=streams[i])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i

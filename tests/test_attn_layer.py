@@ -6,6 +6,10 @@ is checked against the definition in 64 bits, with what the cache holds and what
 """
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -152,3 +156,39 @@ def test_decode_step_replayed_as_one_graph():
         step()
     for (a, b), (x, y) in zip(run(graph.replay), want):
         assert torch.equal(a, x) and torch.equal(b, y)
+
+
+FIRST_CALLS = """
+import torch, linear_attention_token_b200 as gdn
+i32 = dict(dtype=torch.int32, device="cuda")
+B, H_q, H_kv, d = 3, 8, 2, 128
+k = torch.randn(40, 16, H_kv, d, dtype=torch.bfloat16, device="cuda")
+kv = gdn.PagedKV(k, torch.randn_like(k), torch.arange(30, **i32).reshape(B, 10))
+new = torch.randn(B, 1, H_kv, d, dtype=torch.bfloat16, device="cuda")
+q = torch.randn(B, 1, H_q, d, dtype=torch.bfloat16, device="cuda")
+prompt = torch.randn(B, 100, H_q, d, dtype=torch.bfloat16, device="cuda")
+pos, idx = torch.tensor([120, 7, 90], **i32), torch.arange(60, **i32).expand(B, 60).contiguous()
+freq = gdn.rope_inv_freq(d)
+
+def step():
+    turned = gdn.gdn_kv_append(new, new, kv, None, pos, q=q, inv_freq=freq)
+    return (turned, *gdn.gdn_attn_decode(turned, pos, kv), *gdn.gdn_qsa_attn_decode(turned, pos, kv, idx, recent=4),
+            *gdn.gdn_attn_prefill(prompt, kv))
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(captured, step()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: what a first call sets up does not break the capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
