@@ -924,9 +924,10 @@ cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
     attn_decode_kernel<ROWS, D, LIST, false><<<grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = p.rows < ROWS::kRows ? p.rows : ROWS::kRows;
-    // (4 sequences x 2 heads of 1024 tokens: a CTA for each of 296 CTAs and 8 rows 12.3 us a call, for
-    // each unit and row 10.5)
-    const bool few = units * kJoinWarps < grid;
+    // (row to a CTA / to a warp: 1 sequence of 16,384 tokens x 2 heads 13.3 / 28.3 us a call, 4 of 32,768 x 4
+    // 49.8 / 52.4, lists for 40 x 2 heads 22.4 / 23.9; lists for 100 x 2 50.7 / 49.5, 64 x 8 heads of 2048 tokens,
+    // four drafts, 103 / 94)
+    const bool few = units * 3 <= grid;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
