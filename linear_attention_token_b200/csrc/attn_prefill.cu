@@ -186,7 +186,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     auto tiles_of = [&](int i) -> int {                                  // K / V tiles row tile i walks
         const int a = q0 + i * bt_tile;
         const int hi = a < len ? see.hi(min(a + bt_tile, len) - 1) : 0;
-        return hi > k_base ? (hi - k_base + kTile - 1) / kTile : 0;
+        return hi > k_base ? (hi - k_base - 1) / kTile + 1 : 0;
     };
     int tiles_a = tiles_of(0), tiles_b = tiles_of(1), nt = max(tiles_a, tiles_b);
     int parts = 1;
@@ -247,7 +247,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             float s[128];
 #pragma unroll
             for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
-            const bool whole = k0 >= lo_max && k0 + kTile <= hi_min &&
+            const bool whole = k0 >= lo_max && k0 <= hi_min - kTile &&
                                (pm.x & pm.y & pm.z & pm.w) == 0xffffffffu;
             uint32_t live[4] = {pm.x, pm.y, pm.z, pm.w};
             if (!whole) {
@@ -530,11 +530,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
             for (int j = 0; ok && j < nt; ++j) {
                 const int k0 = k_base + j * kTile;
-                const int t = k0 + lane * box;
+                const int t = k0 + min(lane, boxes - 1) * box;
                 const int src = lane < boxes && t < e ? cache_row(p.cache, n, t) : -1;
                 const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
                 const uint32_t bytes = __popc(there) * box * D * 2;
-                const bool patch = __popc(there) < boxes || k0 + kTile > e || k0 < k_lo;
+                const bool patch = __popc(there) < boxes || k0 > e - kTile || k0 < k_lo;
                 if (lane < 4) {
                     // presence, 32 tokens a word (a box is at least 16 tokens)
                     const uint32_t a = (there >> (32 * lane / box)) & 1, b = (there >> ((32 * lane + 16) / box)) & 1;

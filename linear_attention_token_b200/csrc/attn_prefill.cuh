@@ -79,14 +79,16 @@ __device__ __forceinline__ Sequence sequence_of(const AttnPrefillParams &p, int 
     return s;
 }
 
-// What the queries of a sequence see: query i sees the tokens [lo(i), hi(i)), both growing with i.
+// What the queries of a sequence see: query i sees the tokens [lo(i), hi(i)), both growing with i and
+// inside [0, e].  e may be the last 32-bit position but 15, so a tile's end may not fit an int: what
+// follows compares distances from a tile's first token, never its end.
 struct Sight {
     long long start;
     int e, pre, window;
     __device__ __forceinline__ Sight(const AttnPrefillParams &p, const Sequence &s) {
         start = s.start;
         e = (int)min(max(start + s.len, 0LL), cache_capacity(p.cache));
-        pre = min(s.pre, e);
+        pre = max(min(s.pre, e), 0);
         window = p.window;
     }
     __device__ __forceinline__ int hi(int i) const {

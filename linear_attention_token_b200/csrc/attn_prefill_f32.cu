@@ -49,17 +49,18 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
     const Sight see(p, seq);
     const long long r0 = (long long)blk * kRows, r_end = (long long)seq.len * p.G;
     const int t_first = (int)(r0 / p.G), t_last = (int)((min(r0 + kRows, r_end) - 1) / p.G);
-    int k_lo = see.lo(t_first), k_hi = see.hi(t_last), parts = 1;
+    const int k_hi = see.hi(t_last);
+    int k_lo = see.lo(t_first), parts = 1;
+    int tiles = k_hi > k_lo ? (k_hi - k_lo - 1) / kKeys + 1 : 0;
     if (p.splits > 1) {
-        const int tiles = k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0;
         parts = split_parts(tiles, p.splits);
         if (split == 0 && tid == 0)
             p.split_blocks[block] = SplitBlock{seq.first, seq.len, blk * kRows, p.G, hk * p.G, parts, 0};
         if (split >= parts) return;
         int from, to;
         split_range(tiles, parts, split, from, to);
-        k_hi = min(k_hi, k_lo + to * kKeys);
         k_lo += from * kKeys;
+        tiles = to - from;
     }
     auto row_at = [&](long long r) -> size_t {
         return (size_t)(seq.first + r / p.G) * p.H_q + (size_t)hk * p.G + r % p.G;
@@ -86,9 +87,10 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
         for (int d = 0; d < D / 32; ++d) o[a][d] = make_float2(0.f, 0.f);
     }
     const float *kc = reinterpret_cast<const float *>(p.cache.k), *vc = reinterpret_cast<const float *>(p.cache.v);
-    for (int k0 = k_lo; k0 < k_hi; k0 += kKeys) {
+    for (int i = 0; i < tiles; ++i) {
+        const int k0 = k_lo + i * kKeys;
         __syncthreads();                                     // the last tile has been used
-        if (tid < kKeys) rows[tid] = k0 + tid < k_hi ? cache_row(p.cache, n, k0 + tid) : -1;
+        if (tid < kKeys) rows[tid] = tid < k_hi - k0 ? cache_row(p.cache, n, k0 + tid) : -1;
         __syncthreads();
         for (int i = tid; i < kKeys * C4; i += kThreads) {
             const int key = i / C4, c = i % C4, row = rows[key];
@@ -133,7 +135,7 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int key = tx + 16 * b;
-                const bool live = k0 + key >= lo[a] && k0 + key < hi[a] && rows[key] >= 0;
+                const bool live = key >= lo[a] - k0 && key < hi[a] - k0 && rows[key] >= 0;
                 s[a][b] = live ? s[a][b] : -INFINITY;
                 mx = fmaxf(mx, s[a][b]);
             }
