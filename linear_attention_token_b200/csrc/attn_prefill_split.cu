@@ -163,12 +163,18 @@ cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int
     p.window = window;
     p.pack_shift = s.pack_shift;
     p.score = scoring(scale, cap);
-    // The bf16 kernel's polynomials for capped scores carry powers of k = scale / cap in their coefficients:
-    // up to the 11th (degree 5, |y| <= 1, and degree 3, |y| <= 1/2) where those stay inside fp32; for
-    // larger caps (from 360 at a scale of 0.09) the 5th (degree 2, |y| <= 1/8).
-    const float k = fabsf(p.score.mul);
-    const bool all = k >= 0x1p-12f && k <= 0x1p10f;
-    p.near_at = all ? 1.f : k >= 0x1p-24f && k <= 0x1p10f ? 0.125f : -1.f;
+    // The bf16 kernel's polynomials for capped scores carry the factors cap2 k^(2i+1), k = scale / cap, in
+    // their coefficients.  Degree 5 (|y| <= 1; degree 3 for |y| <= 1/2) serves where the first and the last
+    // of these, and so all between, are inside fp32 with room for a coefficient below and a sum above
+    // (2^-124: a coefficient that is no longer normal is off by 2^-26 of the whole at most); else degree 2
+    // (|y| <= 1/8; caps from 390 at a scale of 0.09), else none.
+    const double k = fabs((double)p.score.mul), cap2 = p.score.cap2;
+    auto inside = [&](int degree) {
+        const double first = k * cap2, last = first * pow(k, 2 * degree);
+        return fmin(first, last) >= 0x1p-124 && fmax(first, last) <= 0x1p120 && k >= 0x1p-60 && k <= 0x1p60;
+    };
+    const bool all = inside(5);
+    p.near_at = all ? 1.f : inside(2) ? 0.125f : -1.f;
     p.nearer_at = all ? 0.5f : -1.f;
     p.err = static_cast<DeviceError *>(workspace);
     p.budget = budget;

@@ -1,5 +1,11 @@
-"""The paged attention at the ends of what its arguments allow."""
+"""The paged attention at the ends of what its arguments allow: caps and scales that leave little of
+fp32's range, positions at the end of 32 bits, one workspace for every call, and parts of a long
+sequence that each have to arrive.  Inputs are chosen so that the exact answer is known well below a
+kernel's rounding; each tolerance stands beside the roundings it counts (u = 2^-24, half a step of fp32;
+bf16: 2^-8)."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -11,10 +17,39 @@ from attn_ref import attend, cache, check, fill, normal
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
 
 
 def ints(*x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def one_hot(dots, heads, d, dtype, seed=0):
+    """A cache of len(dots) tokens (one key head) whose key t has dots[t] in dim 0 and noise elsewhere, and
+    the values; a query with a power of two in dim 0 and zeros elsewhere then has an exact dot product."""
+    g = torch.Generator().manual_seed(seed)
+    n, page = len(dots), 64
+    pages = -(-n // page)
+    k = torch.zeros(pages, page, 1, d, dtype=dtype, device=DEV)
+    k.view(-1, d)[:n] = torch.randn(n, d, generator=g).to(dtype).to(DEV)
+    k.view(-1, d)[:n, 0] = torch.as_tensor(dots).to(dtype).to(DEV)
+    v = torch.zeros_like(k)
+    v.view(-1, d)[:n] = torch.randn(n, d, generator=g).to(dtype).to(DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    return gdn.PagedKV(k, v, table), k.view(-1, d)[:n, 0].double(), v.view(-1, d)[:n].double()
+
+
+def capped_softmax(dot, seen, v, scale, cap):
+    """The definition in 64 bits: dot [n] or [R, n], seen [R, n] -> out [R, d], lse [R], sum w |v|."""
+    x = (cap * torch.tanh(dot * scale / cap)).masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(x, -1)
+    w = torch.exp(x - lse[:, None])
+    return w @ v, lse, w @ v.abs()
+
+
+def close(got, want, tol, what):
+    e = (got.double() - want).abs()
+    assert bool((e <= tol).all()), f"{what}: off by {float((e / tol).max()):.3g} of its tolerance"
 
 
 # ------------------------------------------------------------------------- the end of 32 bits
@@ -55,3 +90,38 @@ def test_last_positions(page, dtype):
             for h in range(G * H_kv):
                 want = attend(q[0, :, h], k[:, h // G], v[:, h // G], (t <= at) & (t > at - window), d ** -0.5, 0.0, dtype == BF)
                 check(out[0, :, h], lse[0, :, h], want, f"decode {T} x {G}: start {start - end} head {h}")
+
+
+# ------------------------------------------------------------------------------ caps and scales
+@pytest.mark.parametrize("scale,cap", [(1e9, 1e6), (-1e9, 1e6), (2e8, 2e5), (6e9, 1e6), (1e9, 1e5), (30.0, 30.0),
+                                       (1e-3, 20.0), (3e13, 1e6)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_beside_large_scales(scale, cap, d):
+    """Scores on both sides of half the cap, in whole tiles, with scales that no model has.  A score is off
+    by 2^-20 of itself (the cap's polynomials and roundings), and equal dot products of a whole and of a
+    masked tile go through different polynomials, so
+      out  a weight beside another is off by a factor e^dx, dx = 2 2^-20 cap; it is rounded to bf16 for
+           the product (2^-8), the sum takes it unrounded, and out is rounded (2^-8); n u for sums;
+      lse  2^-20 of the largest score, n u of the sum."""
+    n, R, H = 450, 150, 4
+    levels = torch.tensor([0.25, 0.5, 0.625, 0.75, 0.875, 1.0])
+    g = torch.Generator().manual_seed(int(d))
+    dots = levels[torch.randint(0, 6, (n,), generator=g)] * (torch.randint(0, 2, (n,), generator=g) * 2 - 1)
+    dots[::7] = 0.125
+    kv, k0, v = one_hot(dots, H, d, BF)
+    q0 = 2.0 ** math.floor(math.log2(cap / abs(scale)))      # largest |score| 0.5 .. 1 of the cap
+    q = torch.zeros(R, H, d, dtype=BF, device=DEV)
+    q[:, :, 0] = torch.tensor([q0, q0 / 2, -q0, q0 / 4], device=DEV)
+    t = torch.arange(n, device=DEV)
+    seen = t <= torch.arange(n - R, n, device=DEV)[:, None]
+    dx = 2 * 2.0 ** -20 * cap
+    out, lse = gdn.gdn_attn_prefill(q, kv, ints(0, R), ints(n - R), scale=scale, softcap=cap)
+    for h in range(H):
+        o, l, mag = capped_softmax(k0 * float(q[0, h, 0]), seen, v, scale, cap)
+        close(out[:, h], o, (2.0 ** -8 + n * U + math.expm1(dx)) * mag + 2.0 ** -8 * o.abs() + 1e-30, f"out {h}")
+        close(lse[:, h], l, 2.0 ** -20 * (cap + l.abs()) + n * U, f"lse {h}")
+    last, lse1 = gdn.gdn_attn_decode(q[-1:, None].contiguous().view(1, 1, H, d), ints(n - 1), kv, scale=scale, softcap=cap)
+    for h in range(H):
+        o, l, mag = capped_softmax(k0 * float(q[0, h, 0]), seen[-1:], v, scale, cap)
+        close(last[0, :, h], o, (2.0 ** -8 + n * U + math.expm1(dx)) * mag + 2.0 ** -8 * o.abs() + 1e-30, f"decode out {h}")
+        close(lse1[0, :, h], l, 2.0 ** -20 * (cap + l.abs()) + n * U, f"decode lse {h}")
