@@ -23,6 +23,10 @@
  * gets out = 0 and lse = -inf.  Scores, running maxima and sums are fp32; with bf16 inputs
  * the weights exp(x_t - max) are rounded to bf16 for the product with v.
  *
+ * scale is any finite number, without a cap at most 2.3e38 in magnitude (else
+ * GDN_ERR_INVALID_ARG).  Every q . k, and without a cap every scale q . k (2.3e38 at most), of a
+ * visible token must be finite in fp32: a score that overflows is not a number in out and lse.
+ *
  * The cache.  Token t of sequence n is row t % page_size of page
  * page_table[n, t / page_size].  A token is absent (nobody sees it, and appending it writes
  * nothing) when t / page_size >= max_pages or that entry lies outside [0, num_pages), so

@@ -1,5 +1,6 @@
 // libgdn C ABI: argument checks, kernel choice, launch on the caller's stream.
 // The operation and the contract of every entry point are stated in include/gdn.h.
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -508,9 +509,13 @@ int sm_count()
     const int sms = gdn::device_sm_count();
     return sms > 0 ? sms : kDefaultSms;
 }
-// 0, or a cap that neither its quotient with the scale nor its score in base 2 can overflow
+// 0, or a cap whose product with log2 e stays in fp32 (any finite scale beside it: scoring())
 bool softcap_ok(float cap) { return cap == 0.f || (cap >= 1e-4f && cap <= 1e6f); }
-bool scale_ok(float scale) { return scale > -INFINITY && scale < INFINITY; }
+// finite; without a cap also as the factor of scores in base 2
+bool scale_ok(float scale, float cap)
+{
+    return scale > -INFINITY && scale < INFINITY && (cap != 0.f || fabsf(scale) <= 2.3e38f);
+}
 }  // namespace
 
 GDN_API gdn_status gdn_kv_append(const gdn_paged_kv *kv, const void *k, const void *v,
@@ -578,7 +583,7 @@ gdn_status attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *
     if (n_queries < 1 || n_queries > GDN_ATTN_MAX_QUERIES) return GDN_ERR_UNSUPPORTED;
     if (H_q <= 0 || H_q % kv->H_kv != 0) return GDN_ERR_INVALID_ARG;
     if (H_q > kMostHeads) return GDN_ERR_UNSUPPORTED;
-    if (!scale_ok(scale) || !softcap_ok(softcap) || window < 0) return GDN_ERR_INVALID_ARG;
+    if (!softcap_ok(softcap) || !scale_ok(scale, softcap) || window < 0) return GDN_ERR_INVALID_ARG;
     if (lists) {
         if (list_len < 0 || recent < 0) return GDN_ERR_INVALID_ARG;
         if (list_len > GDN_ATTN_MAX_LIST || recent > 65536) return GDN_ERR_UNSUPPORTED;
@@ -645,7 +650,7 @@ GDN_API gdn_status gdn_attn_prefill(const void *q, const gdn_paged_kv *kv,
         return GDN_ERR_INVALID_ARG;
     if (H_q <= 0 || H_q % kv->H_kv != 0) return GDN_ERR_INVALID_ARG;
     if (H_q > kMostHeads) return GDN_ERR_UNSUPPORTED;
-    if (!scale_ok(scale) || !softcap_ok(softcap) || window < 0) return GDN_ERR_INVALID_ARG;
+    if (!softcap_ok(softcap) || !scale_ok(scale, softcap) || window < 0) return GDN_ERR_INVALID_ARG;
     if (window > 0 && prefix_len) return GDN_ERR_UNSUPPORTED;
     if (T_total == 0 || num_seqs == 0) return GDN_OK;
     if (!q || !out) return GDN_ERR_INVALID_ARG;

@@ -65,6 +65,9 @@ struct Scoring {
 inline Scoring scoring(float scale, float cap) {
     Scoring s;
     s.mul = cap > 0.f ? scale / cap : scale * kLog2e;
+    // (a quotient past fp32 becomes its largest number, since infinity times a zero score is none; any
+    // other score is the cap then either way)
+    if (cap > 0.f) s.mul = fminf(fmaxf(s.mul, -3.402823466e38f), 3.402823466e38f);
     s.cap2 = cap * kLog2e;
     return s;
 }

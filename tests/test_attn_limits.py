@@ -125,3 +125,25 @@ def test_caps_beside_large_scales(scale, cap, d):
         o, l, mag = capped_softmax(k0 * float(q[0, h, 0]), seen[-1:], v, scale, cap)
         close(last[0, :, h], o, (2.0 ** -8 + n * U + math.expm1(dx)) * mag + 2.0 ** -8 * o.abs() + 1e-30, f"decode out {h}")
         close(lse1[0, :, h], l, 2.0 ** -20 * (cap + l.abs()) + n * U, f"decode lse {h}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale,cap", [(1e35, 1e-4), (-3e38, 1e-4), (3e38, 1.0)])
+def test_zero_scores_beside_quotients_past_fp32(scale, cap, dtype):
+    """scale / cap does not fit fp32: a score is 0 where the dot product is, and the cap with its sign
+    elsewhere.  out: weights and result rounded (bf16 2^-8, fp32 8 u: exponential 4 u, sums n u); lse the
+    same beside a score of at most 1."""
+    n, H, d = 300, 2, 64
+    dots = torch.tensor([0.0, 1.0, -1.0, 0.5, 0.0])[torch.arange(n) % 5]
+    kv, k0, v = one_hot(dots, H, d, dtype)
+    q = torch.zeros(2, H, d, dtype=dtype, device=DEV)
+    q[:, 1, 0] = 2.0                                         # head 0: every dot product is 0
+    seen = torch.arange(n, device=DEV) <= torch.tensor([[n - 2], [n - 1]], device=DEV)
+    half = 2.0 ** -8 if dtype == BF else U
+    got = [gdn.gdn_attn_prefill(q, kv, ints(0, 2), ints(n - 2), scale=scale, softcap=cap),
+           [x[0] for x in gdn.gdn_attn_decode(q[None], ints(n - 2), kv, scale=scale, softcap=cap)]]
+    for out, lse in got:
+        for h in range(H):
+            o, l, mag = capped_softmax(k0 * 2.0 * h, seen, v, scale, cap)
+            close(out[:, h], o, (half + (n + 40) * U) * mag + half * o.abs() + 1e-30, f"out {h}")
+            close(lse[:, h], l, (n + 40) * U + 4 * U * l.abs(), f"lse {h}")
