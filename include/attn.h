@@ -95,10 +95,12 @@ gdn_status gdn_kv_append(const gdn_paged_kv *kv, const void *k, const void *v, c
                          const int32_t *rope_pos, const int32_t *rope_sections, int32_t n_axes,
                          uint32_t flags, cudaStream_t stream);
 
-/* Bytes of device workspace the two decode calls need on the current device (no initial
- * contents required; calls that share one must not overlap on the GPU).  It does not depend
- * on the lengths, so a captured graph can be replayed as the sequences grow.  0 for sizes
- * the calls refuse. */
+/* Bytes of device workspace the two decode calls need on the current device.  The first 16
+ * bytes are the device error word, as in gdn.h: zero-fill them before first use for
+ * gdn_get_device_error to be read; the calls write there nothing but an error, and need no other
+ * contents, so one workspace can serve decode calls and prompts in turn.  Calls that share one must
+ * not overlap on the GPU.  The size does not depend on the lengths, so a captured graph can be
+ * replayed as the sequences grow.  0 for sizes the calls refuse. */
 size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, int32_t H_kv, int32_t d,
                                       gdn_dtype dtype);
 
@@ -110,7 +112,7 @@ size_t gdn_attn_decode_workspace_size(int32_t n_queries, int32_t H_q, int32_t H_
  *   lse      : [num_seqs, n_queries, H_q] fp32 or NULL
  * The tokens' keys and values, the queries' own among them, are in the cache already.
  * (Many drafted tokens of wide groups run on gdn_attn_prefill's bf16 kernel, with its bounded
- * waits: a workspace whose first 16 bytes are zero records a timeout for gdn_get_device_error.) */
+ * waits: a timeout is recorded in the workspace's error word.) */
 gdn_status gdn_attn_decode(const void *q, const int32_t *q_pos, const gdn_paged_kv *kv,
                            void *out, float *lse, int32_t num_seqs, int32_t n_queries,
                            int32_t H_q, float scale, float softcap, int32_t window,

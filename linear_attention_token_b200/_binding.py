@@ -593,10 +593,12 @@ def gdn_attn_decode_workspace_size(n_queries: int, H_q: int, H_kv: int, d: int,
 
 def attn_decode_workspace(n_queries: int, H_q: int, H_kv: int, d: int, dtype=torch.bfloat16,
                           device="cuda") -> torch.Tensor:
-    """A workspace for gdn_attn_decode and gdn_qsa_attn_decode (any contents).  Calls that may
-    overlap on the GPU need one each."""
+    """A workspace for gdn_attn_decode and gdn_qsa_attn_decode, its error word zero-filled (the rest
+    may hold anything).  Calls that may overlap on the GPU need one each."""
     n = gdn_attn_decode_workspace_size(n_queries, H_q, H_kv, d, dtype)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace[:256].zero_()
+    return workspace
 
 
 def gdn_attn_decode(q, q_pos, kv: PagedKV, *, scale: Optional[float] = None, softcap: float = 0.0,

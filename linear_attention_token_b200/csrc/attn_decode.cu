@@ -918,7 +918,7 @@ cudaError_t launch_rows(DecodeParams p, void *workspace, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, attn_decode_kernel<ROWS, D, LIST, true>, p);
     }
     p.by_unit = units <= grid;
-    p.rec = static_cast<JoinRecord *>(workspace);
+    p.rec = reinterpret_cast<JoinRecord *>(static_cast<unsigned char *>(workspace) + kErrorBytes);
     p.part_ml = reinterpret_cast<float2 *>(p.rec + grid);
     p.part_o = reinterpret_cast<float *>(p.part_ml + (size_t)grid * 2 * ROWS::kRows);
     attn_decode_kernel<ROWS, D, LIST, false><<<grid, kThreads, smem, stream>>>(p);
@@ -974,11 +974,14 @@ cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int
                                 void *workspace, size_t workspace_bytes, int sms, uint32_t budget,
                                 cudaStream_t stream);
 
-// `rows`: query rows that share a key head (H_q / H_kv x n_queries), blocked as launch_dim does
+// `rows`: query rows that share a key head (H_q / H_kv x n_queries), blocked as launch_dim does.  Records
+// and parts come behind the error word, which the prompt kernel and gdn_get_device_error take to be at the
+// start of any workspace: a share more than the SMs' makes room for it.
 size_t attn_decode_workspace_bytes(int rows, int d, int sms) {
     const size_t block = rows <= 16 ? 16 : rows <= 32 ? 32 : kMostRows;
-    const size_t own = (size_t)sms * kCtasPerSm *
-                       (sizeof(JoinRecord) + 2 * block * (sizeof(float2) + d * sizeof(float)));
+    const size_t share = kCtasPerSm * (sizeof(JoinRecord) + 2 * block * (sizeof(float2) + d * sizeof(float)));
+    static_assert(kErrorBytes <= kCtasPerSm * 2 * 16 * sizeof(float2), "the error word fits the least share");
+    const size_t own = (size_t)(sms + 1) * share;
     // (a call that the prompt kernel takes needs a little more for its table of blocks)
     return rows > 32 ? own + ((size_t)64 << 10) : own;
 }

@@ -82,8 +82,6 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
     if (lane == 0 && p.lse) p.lse[rh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-constexpr size_t kErrorBytes = 256;        // the error word, padded
-
 struct Shape {
     int pack_shift, rows, splits;          // heads packed into a row tile (bf16), rows of a block
     long long blocks;                      // (block, head) pairs, at most

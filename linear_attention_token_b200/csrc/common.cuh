@@ -9,7 +9,7 @@
 
 namespace gdn {
 
-// Device error word layout (first 16 bytes of the prefill workspace):
+// Device error word layout (first 16 bytes of a workspace of gdn_prefill or the attention calls):
 //   word[0] = first gdn_status recorded (0 = none), word[1] = where it happened,
 //   word[2] = blockIdx.x, word[3] = blockIdx.y of the recording CTA.
 struct DeviceError {

@@ -306,7 +306,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     at::Tensor made_out, made_lse;
     if (!out) { made_out = empty(q.sizes(), kv.dtype, kv); out = &made_out; }
     if (!lse && want) { made_lse = empty({seqs, T, heads}, at::kFloat, kv); lse = &made_lse; }
-    if (!ws) {
+    if (!ws) {                             // (its error word, which nobody could read, is left as it is)
         const size_t bytes = gdn_attn_decode_workspace_size((int32_t)T, (int32_t)heads, kv.c.H_kv, kv.c.d, kv.c.dtype);
         s.made = empty({(int64_t)bytes}, at::kByte, kv);
         s.at = s.made.data_ptr();

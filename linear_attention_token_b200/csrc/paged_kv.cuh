@@ -6,6 +6,8 @@
 
 namespace gdn {
 
+constexpr size_t kErrorBytes = 256;        // the error word at a workspace's start, padded
+
 struct PagedView {
     unsigned char *k, *v;
     const int32_t *table;          // [num_seqs, max_pages]

@@ -147,3 +147,39 @@ def test_zero_scores_beside_quotients_past_fp32(scale, cap, dtype):
             o, l, mag = capped_softmax(k0 * 2.0 * h, seen, v, scale, cap)
             close(out[:, h], o, (half + (n + 40) * U) * mag + half * o.abs() + 1e-30, f"out {h}")
             close(lse[:, h], l, (n + 40) * U + 4 * U * l.abs(), f"lse {h}")
+
+
+# ----------------------------------------------------------------------------------- one workspace
+def zeros_cache(N, H_kv, d, tokens, dtype=BF):
+    k = torch.zeros(4, 64, H_kv, d, dtype=dtype, device=DEV)
+    table = (torch.arange(N * (tokens // 64), dtype=torch.int32, device=DEV) % 4).view(N, -1)
+    return gdn.PagedKV(k, torch.zeros_like(k), table)
+
+
+def test_decode_leaves_the_error_word_alone():
+    """One zeroed workspace: an even split of more units than CTAs, then drafts on the prompt kernel with
+    no polls allowed, then both again.  Only the call that gave up is reported, and is."""
+    many = zeros_cache(700, 1, 64, 512), torch.zeros(700, 1, 4, 64, dtype=BF, device=DEV)
+    wide = zeros_cache(8, 1, 64, 512), torch.zeros(8, 8, 16, 64, dtype=BF, device=DEV)
+    n = max(gdn.gdn_attn_decode_workspace_size(q.shape[1], q.shape[2], 1, 64) for _, q in (many, wide))
+    ws = gdn.attn_decode_workspace(8, 16, 1, 64)             # the larger of the two
+    assert ws.numel() == n
+
+    def call(kv, q):
+        at = torch.full((q.shape[0],), 512 - q.shape[1], dtype=torch.int32, device=DEV)
+        gdn.gdn_attn_decode(q, at, kv, workspace=ws)
+        return gdn.gdn_get_device_error(ws)
+
+    assert call(*many) == gdn.GDN_OK
+    assert call(*wide) == gdn.GDN_OK
+    old = gdn.gdn_set_wait_budget(0)
+    try:
+        assert call(*wide) == gdn.GDN_ERR_TIMEOUT
+    finally:
+        gdn.gdn_set_wait_budget(old)
+    assert call(*many) == gdn.GDN_OK
+    assert call(*wide) == gdn.GDN_OK
+    kv, q = wide                                             # and a prompt on the same scratch
+    call(*many)
+    gdn.gdn_attn_prefill(q, kv, None, None, workspace=ws)
+    assert gdn.gdn_get_device_error(ws) == gdn.GDN_OK
