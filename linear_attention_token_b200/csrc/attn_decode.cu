@@ -19,7 +19,8 @@
 //    one, joins them.  (The last CTA of a unit joining in this kernel was slower on every size: one
 //    CTA's fences, atomics and cold code at the end cost more than a second grid.)
 //    Short calls of few units take a cluster of CTAs to a unit instead, which join their parts in
-//    shared memory and need no second grid (cluster_for).
+//    shared memory and need no second grid (cluster_for); drafts of many rows behind a short table
+//    the prompt kernel (many_rows).
 //  - bf16: a warp owns 16 query rows as one mma.sync m16n8k16 row tile.  With few rows the
 //    product is far from the tensor pipe's limit, so what counts is that loads never pause:
 //    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
@@ -41,6 +42,9 @@
 #include "sm100.cuh"
 
 namespace gdn {
+// CTAs that share a block of a dense call of the prompt kernel when its table holds a long context
+int attn_prefill_splits(const gdn_paged_kv &kv, int N, long long T_total, int H_q, int sms);
+
 using sm100::cluster_rank;
 using sm100::cluster_size;
 using sm100::cluster_sync;
@@ -955,15 +959,29 @@ cudaError_t launch_dim(const DecodeParams &p, bool bf16, void *ws, cudaStream_t 
 
 constexpr int kMostRows = 64;              // largest ROWS::kRows
 
-// Whether a call's drafted tokens make enough rows for the prompt kernel (attn_prefill.cu), whose
-// tcgen05 products take 128 rows at the pace of one.  With more than 32 rows to a block of it, mma.sync
-// row tiles no longer keep up with the cache (64 sequences x 2 heads x 4096 tokens, 64 rows: 91
-// against 60 us, 128 rows: 162 against 60; 32 rows: 60 both); with fewer than 8 units the even split
-// over all SMs wins all the same (1 sequence x 2 heads x 8000 tokens, 64 rows: 19 against 24 us).
-bool many_rows(int N, int T, int H_kv, int G) {
+// Query rows that share a block of the prompt kernel (attn_prefill.cu): drafted tokens x packed heads.
+int block_rows(int T, int G) {
     int pack = 1;
     while (pack < 16 && G % (2 * pack) == 0) pack *= 2;
-    return T * pack > 32 && (long long)N * H_kv >= 8;
+    return T * pack;
+}
+
+// Whether a call's drafted tokens make enough rows for the prompt kernel, whose tcgen05 products take 128
+// rows at the pace of one.  With more than 32 rows to a block of it, mma.sync row tiles no longer keep up
+// with the cache; with fewer than 8 units the even split over all SMs wins all the same (1 sequence x 2
+// heads x 8000 tokens, 64 rows: 19 against 24 us).
+// That kernel gives every block the same CTAs, so the longest sequence sets its time, 12 us for each 1000
+// tokens of a CTA, and lengths are not known here: only calls that cannot leave a CTA more than 64
+// tokens to a row of its block take it, which keeps the loss on a skewed batch at the gain on an even one.
+// (64 sequences x 2 heads, prompt kernel / even split.  At the limit: 64 rows, all of 4096 tokens 59 / 85 us,
+// one among 512s 56 / 29; 128 rows, all of 8192 tokens 108 / 270, one among 1000s 106 / 57.  Past it: one of
+// 262,144 among 1000s, 64 rows 3130 / 126, 128 rows 3140 / 208; 1000 to 32,768 tokens 391 / 290 and 399 / 540.)
+bool many_rows(const gdn_paged_kv &kv, int N, int T, int H_q, int window, int sms) {
+    const int rows = block_rows(T, H_q / kv.H_kv);
+    if (rows <= 32 || (long long)N * kv.H_kv < 8) return false;
+    long long tokens = (long long)kv.max_pages * kv.page_size;
+    if (window > 0 && tokens > (long long)window + T) tokens = (long long)window + T;
+    return tokens <= 64LL * rows * attn_prefill_splits(kv, N, (long long)N * T, H_q, sms);
 }
 
 }  // namespace
@@ -991,7 +1009,7 @@ cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int3
                                void *out, float *lse, int N, int T, int H_q, float scale,
                                float cap, int window, void *workspace, size_t workspace_bytes,
                                int sms, uint32_t budget, cudaStream_t stream) {
-    if (!lists && kv.dtype == GDN_BF16 && many_rows(N, T, kv.H_kv, H_q / kv.H_kv))
+    if (!lists && kv.dtype == GDN_BF16 && many_rows(kv, N, T, H_q, window, sms))
         return launch_attn_prefill(kv, q, nullptr, q_pos, nullptr, out, lse, N, (long long)N * T, H_q,
                                    scale, cap, window, workspace, workspace_bytes, sms, budget, stream);
     DecodeParams p = {};

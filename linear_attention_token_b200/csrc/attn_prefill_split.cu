@@ -137,6 +137,10 @@ size_t attn_prefill_workspace_bytes(const gdn_paged_kv &kv, bool varlen, int N, 
     return s.splits > 1 ? s.bytes() : kErrorBytes;
 }
 
+int attn_prefill_splits(const gdn_paged_kv &kv, int N, long long T_total, int H_q, int sms) {
+    return prefill_shape(kv, false, N, T_total, H_q, sms).splits;
+}
+
 cudaError_t launch_attn_prefill(const gdn_paged_kv &kv, const void *q, const int32_t *cu,
                                 const int32_t *pos0, const int32_t *prefix, void *out, float *lse,
                                 int N, long long T_total, int H_q, float scale, float cap, int window,

@@ -183,3 +183,38 @@ def test_decode_leaves_the_error_word_alone():
     call(*many)
     gdn.gdn_attn_prefill(q, kv, None, None, workspace=ws)
     assert gdn.gdn_get_device_error(ws) == gdn.GDN_OK
+
+
+@pytest.mark.parametrize("T,G", [(4, 16), (8, 16)])
+def test_wide_tables_keep_the_even_split(T, G):
+    """Drafts of many rows run on the prompt kernel only where no sequence can be far longer than the rest:
+    its waits (none allowed here) give up, the even split has none.  One long sequence among short ones is
+    right either way."""
+    N, H_kv, d = 8, 1, 64
+    q = torch.zeros(N, T, G * H_kv, d, dtype=BF, device=DEV)
+    at = torch.full((N,), 500 - T, dtype=torch.int32, device=DEV)
+    narrow = zeros_cache(N, H_kv, d, 512)
+    wide = gdn.PagedKV(narrow.k, narrow.v, torch.zeros(N, 1 << 15, dtype=torch.int32, device=DEV))
+    ws = gdn.attn_decode_workspace(T, G * H_kv, H_kv, d)
+    old = gdn.gdn_set_wait_budget(0)
+    try:
+        for kv, window, want in ((narrow, 0, gdn.GDN_ERR_TIMEOUT), (wide, 0, gdn.GDN_OK),
+                                 (wide, 1000, gdn.GDN_ERR_TIMEOUT)):
+            gdn.gdn_attn_decode(q, at, kv, window=window, workspace=ws)
+            assert gdn.gdn_get_device_error(ws) == want
+    finally:
+        gdn.gdn_set_wait_budget(old)
+    kv, dots, v = one_hot(torch.tensor([0.0, 1.0, -1.0, 0.5])[torch.arange(20_000) % 4], G, d, BF)
+    table = torch.full((N, 1 << 15), -1, dtype=torch.int32, device=DEV)
+    table[:, :kv.page_table.shape[1]] = kv.page_table
+    lens = [20_000] + [30 + n for n in range(N - 1)]
+    q[..., 0] = 1.0
+    out, lse = gdn.gdn_attn_decode(q, ints(*lens) - T, gdn.PagedKV(kv.k, kv.v, table), scale=1.0)
+    for n, L in enumerate(lens):
+        for j in range(T):
+            x = dots[:L - T + j + 1]
+            want = torch.exp(x - torch.logsumexp(x, 0)) @ v[:len(x)]
+            mag = torch.exp(x - torch.logsumexp(x, 0)) @ v[:len(x)].abs()
+            # weights and result rounded to bf16; exponentials 4 u and the sums n u
+            close(out[n, j], want.expand(G, d), (2.0 ** -8 + (len(x) + 8) * U) * mag + 2.0 ** -8 * want.abs(), f"{n} {j}")
+            close(lse[n, j], torch.logsumexp(x, 0).expand(G), (len(x) + 16) * U, f"lse {n} {j}")
