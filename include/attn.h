@@ -21,7 +21,8 @@
  *
  * over the tokens t that the query sees (each call says which).  A query that sees none
  * gets out = 0 and lse = -inf.  Scores, running maxima and sums are fp32; with bf16 inputs
- * the weights exp(x_t - max) are rounded to bf16 for the product with v.
+ * the weights exp(x_t - max) are rounded to bf16 for the product with v, and the cap is off by up to
+ * 2^-20 of the score.
  *
  * scale is any finite number, without a cap at most 2.3e38 in magnitude (else
  * GDN_ERR_INVALID_ARG).  Every q . k, and without a cap every scale q . k (2.3e38 at most), of a

@@ -265,7 +265,7 @@ struct TensorRows {
                 mma16816(s[2 * i + 1], q[k], b[2], b[3]);
             }
         }
-        score2(reinterpret_cast<float(&)[NT * 4]>(s), p.score);
+        score2<5>(reinterpret_cast<float(&)[NT * 4]>(s), p.score);
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -296,7 +296,7 @@ struct TensorRows {
         const float shift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         // rounded to bf16 for the product (each weight is off by half a step, 2^-8 of itself, at
         // most; over many keys the errors average out below the output's own rounding); the sum
-        // takes the unrounded weights, so lse is exact to fp32
+        // takes the unrounded weights, so lse has no part in it
         uint32_t w[NT / 2][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -400,7 +400,7 @@ struct FmaRows {
 #pragma unroll
             for (int d = 1; d < kLanes; d <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], d);
         }
-        score2(s, p.score);
+        score2<7>(s, p.score);
         const int t = (int)(token0 + key);
         const bool there = (present >> key) & 1;
         bool grow = false;

@@ -289,8 +289,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         s[c + 1] = x.y;
                     }
                 };
-                if (!near) cap_all([&](float2 y) { return capped2(y, cap2); });
-                else if (!whole) cap_all([&](float2 y) { return capped_near2(y, cap2); });
+                if (!near) cap_all([&](float2 y) { return capped2<3>(y, cap2); });
+                else if (!whole) cap_all([&](float2 y) { return capped_near2<5>(y, cap2); });
                 near = near && whole;
             }
             if (!whole) {
@@ -304,7 +304,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
             float mx = max3(fmaxf(mx4[0], s[124]), fmaxf(mx4[1], s[125]),
                             fmaxf(fmaxf(mx4[2], s[126]), fmaxf(mx4[3], s[127])));
-            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped_near2(make_float2(mx * k2, 0.f), cap2).x : mx * k2;
+            if (CAP ? near : mx != -INFINITY) mx = CAP ? capped_near2<5>(make_float2(mx * k2, 0.f), cap2).x : mx * k2;
             const bool grow = mx > m + kLazy;                            // also when m is -inf
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2(m - mx) : 1.f;                // 0 from -inf

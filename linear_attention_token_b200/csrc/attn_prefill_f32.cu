@@ -127,7 +127,7 @@ attn_prefill_f32_kernel(const __grid_constant__ AttnPrefillParams p) {
         for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int b = 0; b < 4; ++b) s[a][b] = s2[a][b].x + s2[a][b].y;
-        score2(reinterpret_cast<float(&)[16]>(s), p.score);
+        score2<7>(reinterpret_cast<float(&)[16]>(s), p.score);
         __syncthreads();                                     // the keys have been used
 #pragma unroll
         for (int a = 0; a < 4; ++a) {

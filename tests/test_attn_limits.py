@@ -149,6 +149,27 @@ def test_zero_scores_beside_quotients_past_fp32(scale, cap, dtype):
             close(lse[:, h], l, (n + 40) * U + 4 * U * l.abs(), f"lse {h}")
 
 
+@pytest.mark.parametrize("rows", [1, 4, 8])
+@pytest.mark.parametrize("most", [1.0, 3.0])
+def test_cap_in_fp32(most, rows):
+    """One token a sequence, so lse is its capped score.  The dot product and its quotient with a cap of 32
+    are exact; then cap2 = 32 log2 e (u), y R(y^2) by the polynomial (4.3 u: y^2 .3, the outermost sum 1,
+    the inner ones .6, coefficients .7, fit .1, the product 1, and the one with cap2 1 more) or
+    1 - 2 / (1 + e^2y) beyond 1 (4.8 u: 2y log2 e, ex2, the sum and the quotient make 3.8 u of the
+    result, the last sum 1), and ln 2 and its product (2 u): 8 u of the score."""
+    N, d, cap = 512, 64, 32.0
+    kv, k0, v = one_hot(torch.ones(64 * N), rows, d, F32)
+    kv = gdn.PagedKV(kv.k, kv.v, torch.arange(N, dtype=torch.int32, device=DEV)[:, None].contiguous())
+    q = torch.zeros(N, 1, rows, d, device=DEV)
+    g = torch.Generator().manual_seed(rows)
+    q[..., 0] = ((torch.rand(N, 1, rows, generator=g) * 2 - 1) * most * cap).to(DEV)
+    want = cap * torch.tanh(q[..., 0].double() / cap)
+    _, lse = gdn.gdn_attn_decode(q, torch.zeros(N, dtype=torch.int32, device=DEV), kv, scale=1.0, softcap=cap)
+    close(lse, want, 8 * U * want.abs() + 1e-30, "decode")
+    _, lse = gdn.gdn_attn_prefill(q, kv, None, None, scale=1.0, softcap=cap)
+    close(lse, want, 8 * U * want.abs() + 1e-30, "prompt")
+
+
 # ----------------------------------------------------------------------------------- one workspace
 def zeros_cache(N, H_kv, d, tokens, dtype=BF):
     k = torch.zeros(4, 64, H_kv, d, dtype=dtype, device=DEV)
