@@ -239,3 +239,44 @@ def test_wide_tables_keep_the_even_split(T, G):
             # weights and result rounded to bf16; exponentials 4 u and the sums n u
             close(out[n, j], want.expand(G, d), (2.0 ** -8 + (len(x) + 8) * U) * mag + 2.0 ** -8 * want.abs(), f"{n} {j}")
             close(lse[n, j], torch.logsumexp(x, 0).expand(G), (len(x) + 16) * U, f"lse {n} {j}")
+
+
+# --------------------------------------------------------------------------------- parts of a join
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("levels", [1, 5])
+@pytest.mark.parametrize("N,H_kv,L", [(1, 1, 120_000), (40, 4, 3000), (400, 1, 1500), (3, 2, 2048)])
+def test_every_step_arrives(N, H_kv, L, levels, dtype):
+    """Every step of 64 keys has a place of its own in out and a weight of 2^-j (j < levels) in the sum, so
+    that a step lost or joined twice shows in both: 1 sequence over every SM, units joined by warps, units
+    recorded by CTA, and clusters.
+
+    Weights are within 4 j ln 2 u + 4 u of 2^-j (scale, log2 e, their product and the one with the dot
+    product; the exponential), a part's weight within 4 u; a sum goes through at most 100 roundings (48 of a
+    lane, its row's lanes and the teams; 37 parts of a warp, the warps): 120 u < 2^-17 in all.  In lse also
+    log2 and ln 2, 4 u of it; in out the weights' and its own rounding to its type."""
+    d, steps = 128, -(-L // 64)
+    j = torch.arange(steps) * 7 % levels                     # exponent of a step
+    t = torch.arange(L)
+    G = 2
+    pages = -(-L // 64)
+    k = torch.zeros(pages, 64, H_kv, d, dtype=dtype, device=DEV)
+    v = torch.zeros_like(k)
+    k.view(-1, H_kv, d)[:L, :, 0] = -j[t // 64].to(dtype).to(DEV)[:, None]
+    rows = torch.arange(L, device=DEV)
+    v.view(-1, H_kv, d)[rows, :, (rows // 64) % d] = 1.0
+    kv = gdn.PagedKV(k, v, torch.arange(pages, dtype=torch.int32, device=DEV).expand(N, pages).contiguous())
+    q = torch.zeros(N, 1, G * H_kv, d, dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    at = torch.full((N,), L - 1, dtype=torch.int32, device=DEV)
+    out, lse = gdn.gdn_attn_decode(q, at, kv, scale=math.log(2.0))
+    share = torch.tensor([min(64, L - 64 * s) for s in range(steps)], dtype=torch.float64) * 2.0 ** -j.double()
+    total = share.sum()
+    want = torch.zeros(d, dtype=torch.float64).index_add_(0, torch.arange(steps) % d, share) / total
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    tol, tol_lse = (2 * half + 2.0 ** -17) * want, 2.0 ** -17 + 2.0 ** -22 * math.log(float(total))
+    # the oracle without one step, or with one twice, is out of tolerance, whichever it is
+    for sign in (-1.0, 1.0):
+        other = total + sign * share
+        assert bool(((other.log() - total.log()).abs() > 2 * tol_lse).all())
+    close(lse, total.log().to(DEV).expand_as(lse), tol_lse, "lse")
+    close(out, want.to(DEV).expand_as(out), tol.to(DEV) + 1e-30, "out")
