@@ -280,3 +280,36 @@ def test_every_step_arrives(N, H_kv, L, levels, dtype):
         assert bool(((other.log() - total.log()).abs() > 2 * tol_lse).all())
     close(lse, total.log().to(DEV).expand_as(lse), tol_lse, "lse")
     close(out, want.to(DEV).expand_as(out), tol.to(DEV) + 1e-30, "out")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("levels", [1, 5])
+def test_every_tile_arrives_in_split_prompts(levels, dtype):
+    """The same for a prompt that is split over the context: every query sees every token (a prefix), a tile of
+    128 tokens has a place and a share of its own.  A sum goes through at most 140 roundings (fp32: 4 keys of
+    a tile a lane, 25 tiles of 64 a part; bf16: 32 pairs of a tile, 32 tiles a part; lanes, parts): with the
+    weights' 20 u, 160 u < 2^-16."""
+    d, L, R, G = 128, 100_000, 40, 2
+    steps = -(-L // 128)
+    j = torch.arange(steps) * 7 % levels
+    rows = torch.arange(L, device=DEV)
+    pages = -(-L // 64)
+    k = torch.zeros(pages, 64, 1, d, dtype=dtype, device=DEV)
+    v = torch.zeros_like(k)
+    k.view(-1, d)[:L, 0] = -j.to(dtype).to(DEV)[rows // 128]
+    v.view(-1, d)[rows, (rows // 128) % d] = 1.0
+    kv = gdn.PagedKV(k, v, torch.arange(pages, dtype=torch.int32, device=DEV)[None])
+    q = torch.zeros(R, G, d, dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    assert gdn.gdn_attn_prefill_workspace_size(kv, 1, R, G) > 256          # split
+    out, lse = gdn.gdn_attn_prefill(q, kv, ints(0, R), ints(L - R), prefix_len=ints(L), scale=math.log(2.0))
+    share = torch.tensor([min(128, L - 128 * s) for s in range(steps)], dtype=torch.float64) * 2.0 ** -j.double()
+    total = share.sum()
+    want = torch.zeros(d, dtype=torch.float64).index_add_(0, torch.arange(steps) % d, share) / total
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    tol, tol_lse = (2 * half + 2.0 ** -16) * want, 2.0 ** -16 + 2.0 ** -22 * math.log(float(total))
+    for sign in (-1.0, 1.0):
+        other = total + sign * share
+        assert bool(((other.log() - total.log()).abs() > 2 * tol_lse).all())
+    close(lse, total.log().to(DEV).expand_as(lse), tol_lse, "lse")
+    close(out, want.to(DEV).expand_as(out), tol.to(DEV) + 1e-30, "out")
