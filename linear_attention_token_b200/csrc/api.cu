@@ -58,7 +58,7 @@ cudaError_t launch_kv_append(const gdn_paged_kv &kv, const void *k, const void *
                              long long q_stride, const int32_t *cu, const int32_t *pos0,
                              int num_seqs, long long T_total, int H_q, const float *inv_freq,
                              int rope_dims, const int32_t *rope_pos, const int32_t *sections,
-                             int n_axes, bool interleaved, cudaStream_t stream);
+                             int n_axes, bool interleaved, int sms, cudaStream_t stream);
 size_t attn_decode_workspace_bytes(int rows, int d, int sms);
 cudaError_t launch_attn_decode(const gdn_paged_kv &kv, const void *q, const int32_t *q_pos,
                                const int32_t *list, int list_len, int recent, bool lists,
@@ -557,7 +557,7 @@ GDN_API gdn_status gdn_kv_append(const gdn_paged_kv *kv, const void *k, const vo
     const cudaError_t e = gdn::launch_kv_append(
         *kv, k, v, q, q_out, k_stride, v_stride, q_stride, cu_seqlens, pos0, num_seqs, T_total,
         H_q, inv_freq, rope_dims, rope_pos, rope_sections, n_axes,
-        (flags & GDN_ROPE_INTERLEAVED) != 0, stream);
+        (flags & GDN_ROPE_INTERLEAVED) != 0, sm_count(), stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHalf = 64;           // largest rope_dims / 2
-constexpr int kFewWarps = 148 * 32;    // below this many warps a token is shared by several
+constexpr int kFewWarps = 32;          // below this many warps an SM a token is shared by several
 
 struct AppendParams {
     PagedView cache;
@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 6 : 5) kv_append_kerne
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(AppendParams p, cudaStream_t stream) {
+cudaError_t launch_typed(AppendParams p, int sms, cudaStream_t stream) {
     // warps per token: enough that a few tokens still spread over the SMs, no more than have items
     const int items = (p.H_q + 2 * p.cache.H_kv) * D / (2 * Pack<T>::kN);
-    while (p.split_shift < 3 && (p.T_total << p.split_shift) < kFewWarps &&
+    while (p.split_shift < 3 && (p.T_total << p.split_shift) < (long long)sms * kFewWarps &&
            (32 << p.split_shift) < items)
         ++p.split_shift;
     const long long warps = p.T_total << p.split_shift;
@@ -228,7 +228,7 @@ cudaError_t launch_kv_append(const gdn_paged_kv &kv, const void *k, const void *
                              long long q_stride, const int32_t *cu, const int32_t *pos0,
                              int num_seqs, long long T_total, int H_q, const float *inv_freq,
                              int rope_dims, const int32_t *rope_pos, const int32_t *sections,
-                             int n_axes, bool interleaved, cudaStream_t stream) {
+                             int n_axes, bool interleaved, int sms, cudaStream_t stream) {
     const int esize = kv.dtype == GDN_BF16 ? 2 : 4;
     AppendParams p = {};
     p.cache = paged_view(kv);
@@ -252,9 +252,9 @@ cudaError_t launch_kv_append(const gdn_paged_kv &kv, const void *k, const void *
     for (int a = 0; a < GDN_ROPE_MAX_AXES; ++a) p.sec[a] = sections && a < n_axes ? sections[a] : 0;
     p.interleaved = interleaved;
     if (kv.dtype == GDN_BF16)
-        return kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(p, stream)
-                           : launch_typed<__nv_bfloat16, 64>(p, stream);
-    return kv.d == 128 ? launch_typed<float, 128>(p, stream) : launch_typed<float, 64>(p, stream);
+        return kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(p, sms, stream)
+                           : launch_typed<__nv_bfloat16, 64>(p, sms, stream);
+    return kv.d == 128 ? launch_typed<float, 128>(p, sms, stream) : launch_typed<float, 64>(p, sms, stream);
 }
 
 }  // namespace gdn
