@@ -88,7 +88,7 @@ typedef struct {
  *                GDN_ROPE_INTERLEAVED frequency i belongs to axis a = i % n_axes as long as
  *                i < n_axes * rope_sections[a], else to axis 0.
  * Pointers 16-byte aligned (the int32 and fp32 tables 4), strides multiples of 16 bytes.
- * If two tokens of a call fall on the same row, which one stays is not defined. */
+ * If two tokens of a call fall on the same row, what it holds then is not defined (parts of both). */
 gdn_status gdn_kv_append(const gdn_paged_kv *kv, const void *k, const void *v, const void *q,
                          void *q_out, int64_t k_stride, int64_t v_stride, int64_t q_stride,
                          const int32_t *cu_seqlens, const int32_t *pos0, int32_t num_seqs,
