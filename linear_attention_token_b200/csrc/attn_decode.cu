@@ -25,14 +25,19 @@
 //    product is far from the tensor pipe's limit, so what counts is that loads never pause:
 //    each team of warps (1, 2 or 4 by the number of rows) streams its own keys through a
 //    private ring of cp.async stages and waits for nobody else.
-//  - fp32: the same skeleton with fp32 FMAs (1e-4 rules out reduced-precision operands).
+//  - fp32: the same skeleton with fp32 FMAs (one product of operands of fewer bits would not hold 1e-4).
 //
 // Measured (cache bytes over time; a plain copy moves 6.45 TB/s): 8 sequences of 262,144 tokens x 2 heads
 // bf16 320 us, 6.7 TB/s; 64 ragged ones of 2000 to 16,384 tokens x 8 heads, two drafted tokens each, 356 us,
-// 6.6 TB/s; one of 262,144 tokens x 2 heads 53 us, 5.1 TB/s; fp32, 64 x 4096 tokens x 2 heads, d = 128:
-// 87 us, 6.2 TB/s with one row a head, 126 with eight, which are bound by their FMAs. Lists of 2048 tokens
-// for 32 x 4 drafted queries: 55 us, 4.9 TB/s; 4 x 1024 tokens: 6.6 us, mostly the launch and the chain
-// position -> page table -> keys.
+// 6.6 TB/s; one of 262,144 tokens x 2 heads 53 us, 5.1 TB/s; d = 64, 64 x 8192 tokens x 8 heads 183 us, 5.9
+// TB/s. 64 x 16,384 tokens x 8 heads with a window of 1024: 51 us, 5.2 TB/s, of 4096: 164, 6.5. Lists of
+// 2048 tokens for 32 x 4 drafted queries: 55 us, 4.9 TB/s, in fp32 150, 3.7 TB/s, d = 64 40, 3.4; 4 x 1024
+// tokens: 6.6 us, mostly the launch and the chain position -> page table -> keys.
+// Where it is not the bytes: bf16, 17 to 32 rows (64 x 4096 x 2 heads, 32 rows: 60 us, 4.5 TB/s; 16 rows 54): two warps
+// read each tile whole by ldmatrix, 255 registers leave 8 warps an SM, and 61% of the cycles have none
+// that can issue (tensor pipe 32%). fp32, the same tokens: 84 us with one row a head, 6.4 TB/s; 99 with four;
+// 129 with eight, 17 TFLOP/s: the ring of d = 128 leaves one CTA of four warps an SM, and 69% of the
+// cycles have none that can issue (FMA pipe 29%).
 #include <math.h>
 #include <stdint.h>
 
@@ -890,6 +895,8 @@ template <bool LIST> long long most_steps(const DecodeParams &p) {
 // its length, and some SMs none. (bf16, 16 x 2 heads, even split / cluster: 4 sequences of 1024 tokens 9.5 /
 // 6.6 us; lists of 2048 for 8 sequences 11.1 / 10.1, for 16 14.5 / 11.1, for 32 20.2 / 16.0, for 74 36.8 /
 // 33.2; but for 37 19.8 / 22.4, and 1 sequence of 16,384 tokens 13.4 / 15.9.)
+// The table's width stands for the lengths: 4 sequences of 1024 tokens behind a table of 8192 take 7.2 us, and
+// behind wider ones, where a sequence could be long, the even split's 9.4.
 template <class ROWS, int D, bool LIST> int cluster_for(const DecodeParams &p, long long units, int grid) {
     int dev;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;

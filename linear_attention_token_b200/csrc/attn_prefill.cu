@@ -31,7 +31,9 @@
 //
 // Measured: one prompt of 16,384 tokens x 16 heads (2 key heads) 855-910 us, 1.21-1.29 PFLOP/s on a
 // chip at its power cap (cuBLAS there: 1.40); 2 x 4096 tokens 126 us, 1.09 PFLOP/s, tensor pipe active
-// 49%; 8191 ragged tokens behind 2800-4000, 16 x 4 heads, capped, pages of 16: 398 us. Of these the cap
+// 49%; d = 64: 16,384 tokens 726 us, 0.76 PFLOP/s, 2 x 4096 111 us, 0.62, with as many exponentials
+// (that pipe active 61%) for half the products; a window of 1024 over 16,384 tokens 176 us, 0.76 PFLOP/s;
+// 8191 ragged tokens behind 2800-4000, 16 x 4 heads, capped, pages of 16: 398 us. Of these the cap
 // takes 60 (the FMA pipe), pages of 16 rather than 128 tokens 30 (eight loads to a tile half), and
 // unequal blocks on 148 SMs 40.
 #include <cuda.h>

@@ -8,7 +8,8 @@
 // second kernel.  A CTA takes at least kSplitTiles tiles: below that the fp32 parts and the second
 // launch cost more than the shorter walk saves.  The host knows no lengths, only what the page
 // table can hold: a block that turns out short is run whole by its first CTA, and the join passes
-// over it.
+// over it (a short prompt behind a wide table: 64 tokens x 16 x 2 heads 11.4 us for 10.1, 333 15.1 for 13.5,
+// 700 20.8 for 19.8, and up to 20 MB of workspace).
 #include <math.h>
 #include <stdint.h>
 
@@ -92,7 +93,9 @@ struct Shape {
 Shape prefill_shape(const gdn_paged_kv &kv, bool varlen, int N, long long T_total, int H_q, int sms) {
     Shape s = {};
     const int G = H_q / kv.H_kv;
-    auto bound = [&](long long total, long long size) {       // one block of a sequence may be part full
+    // one block of a sequence may be part full (packed tokens that fill their blocks are counted one block a
+    // sequence too many, whose CTAs leave at once: 64 x 16 x 2 heads behind 100,000 runs on 96 of 148 SMs, 82 us)
+    auto bound = [&](long long total, long long size) {
         return varlen ? total / size + N : (total / N + size - 1) / size * N;
     };
     const bool f32 = kv.dtype == GDN_F32;
